@@ -9,6 +9,14 @@ streams.
     out = gemm(w, x, m, "q4_k")            # dst[n, m] = x[n, k] @ deq(w)[m, k]^T
     g, u = moe_gateup(wg, wu, ids, scales, x, n_expert, n_ff, "nvfp4")
 
+and, between a decode step's projections,
+
+    y, h = add_rmsnorm(x, weight, residual)
+    lens, slots, positions, used = paged_extend(block_table, cached, new, free, page_size, n_rows)
+    cache = KVCache(k_pages, v_pages)      # kept; views of the caller's memory
+    kv_append(cache, k, v, slots)
+    out = paged_attention(q, cache, block_table, lens)
+
 If the library has not been built, every call raises RuntimeError: there is
 no fallback path.
 """
@@ -24,11 +32,14 @@ __all__ = [
     "plan_kernel_name", "moe_gateup", "moe_down", "moe_gateup_act", "moe_gateup_act_q8", "moe_gateup_probe",
     "moe_down_q8",
     "stream_loadonly", "repack_nvfp4_v2", "quantize_q8_1", "moe_gateup_q8",
+    "KV_KINDS", "KVCache", "paged_extend", "kv_append", "paged_attention", "paged_attention_workspace_bytes",
+    "add_rmsnorm", "add_rmsnorm_q8",
     "row_bytes", "block_elems", "gemv_max_n", "status_str", "abi_version",
 ]
 
 QTYPES = {"f32": 0, "q4_0": 1, "q8_0": 2, "q4_k": 3, "q6_k": 4, "nvfp4": 5, "nvfp4_v2": 6}
 PATHS = {"auto": 0, "gemv": 1, "mfma": 2, "gemv_fma": 3, "gemv_matrix": 4}
+KV_KINDS = {"f16": 0, "bf16": 1, "q8": 2}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -97,6 +108,18 @@ def load() -> ctypes.CDLL:
         lib.qmm_nvfp4_repack_v2.restype = i32
         lib.qmm_stream_loadonly.argtypes = [vp, vp, i64, i64, i32, vp]
         lib.qmm_stream_loadonly.restype = i32
+        lib.qmm_paged_extend.argtypes = [vp, i64] + [vp] * 7 + [i64] * 5 + [vp]
+        lib.qmm_paged_extend.restype = i32
+        lib.qmm_kv_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp]
+        lib.qmm_kv_append.restype = i32
+        lib.qmm_paged_attention.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, i64, i64, f32, vp, i64, vp]
+        lib.qmm_paged_attention.restype = i32
+        lib.qmm_paged_attention_workspace_bytes.argtypes = [i64] * 6
+        lib.qmm_paged_attention_workspace_bytes.restype = i64
+        lib.qmm_add_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, f32, vp]
+        lib.qmm_add_rmsnorm.restype = i32
+        lib.qmm_add_rmsnorm_q8.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, f32, vp]
+        lib.qmm_add_rmsnorm_q8.restype = i32
         lib.qmm_row_bytes.argtypes = [i32, i64]
         lib.qmm_row_bytes.restype = i64
         lib.qmm_block_elems.argtypes = [i32]
@@ -512,3 +535,305 @@ def stream_loadonly(w, m: int, k: int, qtype, sink=None, stream=None):
     if st != 0:
         raise QmmError(st, "qmm_stream_loadonly")
     return sink
+
+
+# ------------------------------------------------------------------ decode step
+class _KvCacheStruct(ctypes.Structure):
+    """qmm_kv_cache."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] +
+                [(n, ctypes.c_int64) for n in ("n_pages", "n_kv", "page_size", "head_dim", "page_stride", "head_stride",
+                                               "slot_stride", "scale_page_stride", "scale_head_stride",
+                                               "scale_slot_stride")] + [("kind", ctypes.c_int32)])
+
+
+class KVCache:
+    """A paged key-value cache: views k and v [n_pages, n_kv, page_size, head_dim] of the caller's
+    device memory, which the object keeps alive, in any order of pages, heads and tokens with unit
+    stride along head_dim (pages that hold tokens outermost: ``pages.transpose(1, 2)``).
+
+    float16 or bfloat16, or int8 codes with k_scale and v_scale float32 [n_pages, n_kv, page_size].
+    page_size: a power of two; head_dim: a multiple of 32 up to 256."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        kinds = {torch.float16: "f16", torch.bfloat16: "bf16", torch.int8: "q8"}
+        if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or not k.is_cuda or not v.is_cuda:
+            raise TypeError("k and v must be device (cuda/hip) tensors")
+        if k.dtype not in kinds or v.dtype != k.dtype:
+            raise TypeError(f"k and v must both be float16, bfloat16 or int8, got {k.dtype} and {v.dtype}")
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must both be [n_pages, n_kv, page_size, head_dim]")
+        self.kind = kinds[k.dtype]
+        strides = _view_strides(k, 3, "k")
+        if strides != _view_strides(v, 3, "v"):
+            raise ValueError("k and v must have the same strides")
+        scale_strides = (1, 1, 1)
+        if (k_scale is not None or v_scale is not None) != (self.kind == "q8"):
+            raise ValueError("k_scale and v_scale belong to an int8 cache")
+        if self.kind == "q8":
+            for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
+                    raise TypeError(f"{what} must be a float32 device (cuda/hip) tensor")
+                if t.shape != k.shape[:3]:
+                    raise ValueError(f"{what} must be [n_pages, n_kv, page_size]")
+            scale_strides = _view_strides(k_scale, 3, "k_scale", 1)
+            if scale_strides != _view_strides(v_scale, 3, "v_scale", 1):
+                raise ValueError("k_scale and v_scale must have the same strides")
+        self.device = _same_device(k, v, *(() if k_scale is None else (k_scale, v_scale)))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv, self.page_size, self.head_dim = k.shape
+        self._struct = _KvCacheStruct(
+            k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+            None if v_scale is None else v_scale.data_ptr(), *k.shape, *strides, *scale_strides, KV_KINDS[self.kind])
+        self._ptr = ctypes.addressof(self._struct)
+
+
+def _view_strides(t, n: int, what: str, least=None):
+    """Strides of t's first n axes, those of axes of one entry replaced by the smallest that is
+    valid; unit stride along a last axis behind them."""
+    least = t.shape[-1] if least is None else least
+    if t.dim() > n and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what} must have unit stride along head_dim")
+    strides = tuple(t.stride(i) if t.shape[i] > 1 else least for i in range(n))
+    spans = sorted((s, t.shape[i]) for i, s in enumerate(strides) if t.shape[i] > 1)
+    reach = least
+    for stride, count in spans:
+        if stride < reach:
+            raise ValueError(f"{what}'s rows overlap (strides {strides})")
+        reach = stride * (count - 1) + reach
+    return strides
+
+
+def _same_device(*tensors):
+    device = tensors[0].device
+    for t in tensors[1:]:
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    return device
+
+
+def _i32(t, what, shape=None):
+    """Pointer of a contiguous int32 device tensor (of a shape)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        raise TypeError(f"{what} must be an int32 device (cuda/hip) tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _f32_rows(t, what, n, row, heads=0):
+    """(pointer, row stride) of a float32 device tensor [n, row], or [n, heads, row / heads] with
+    its heads side by side; rows any stride apart."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
+        raise TypeError(f"{what} must be a float32 device (cuda/hip) tensor")
+    shape, stride = t.shape, t.stride()
+    if heads and len(shape) == 3:
+        ok = shape == (n, heads, row // heads) and (heads == 1 or stride[1] == row // heads)
+    else:
+        ok = shape == (n, row)
+    if not ok or (shape[-1] > 1 and stride[-1] != 1):
+        want = f"[{n}, {row}]" + (f" or [{n}, {heads}, {row // heads}]" if heads else "")
+        raise ValueError(f"{what} must be {want} with contiguous rows, got {list(shape)} with strides {list(stride)}")
+    return t.data_ptr(), (stride[0] if n > 1 else (row + 3) // 4 * 4)
+
+
+def _table(t, batch, what="block_table"):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        raise TypeError(f"{what} must be an int32 device (cuda/hip) tensor")
+    if t.dim() != 2 or t.shape[0] != batch or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be [{batch}, max_pages] with unit stride along its rows")
+    return t.data_ptr(), t.shape[1], (t.stride(0) if batch > 1 else t.shape[1])
+
+
+class _On:
+    """Makes a tensor's device the current one, where it is not."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        import torch
+        self.guard = None
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _stream_on(device, stream):
+    """Handle of the given stream, or of the device's current one."""
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+
+
+def paged_extend(block_table, cached_lens, new_lens, free_pages, page_size: int, n_rows: int, seq_lens=None,
+                 slots=None, positions=None, pages_used=None, stream=None):
+    """Page tables of a step: gives each sequence (cached_lens tokens in the cache, new_lens more)
+    the pages it newly needs from free_pages, in order, written into block_table (int32
+    [batch, max_pages], in place); returns (seq_lens [batch], slots [n_rows], positions [n_rows],
+    pages_used [1]), all int32.  slots and positions are those of the new tokens' rows, sequence
+    after sequence, -1 behind the last row and (slots) for a sequence that is refused because its
+    table row or the free list is too short: its seq_lens entry stays cached_lens."""
+    import torch
+    lib = load()
+    batch = cached_lens.shape[0]
+    table, max_pages, table_stride = _table(block_table, batch)
+    device = block_table.device
+    new = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
+    seq_lens = new(batch) if seq_lens is None else seq_lens
+    slots = new(n_rows) if slots is None else slots
+    positions = new(n_rows) if positions is None else positions
+    pages_used = new(1) if pages_used is None else pages_used
+    _same_device(block_table, cached_lens, new_lens, free_pages, seq_lens, slots, positions, pages_used)
+    with _On(device):
+        st = lib.qmm_paged_extend(
+            table, table_stride, _i32(seq_lens, "seq_lens", (batch,)), _i32(slots, "slots", (n_rows,)),
+            _i32(positions, "positions", (n_rows,)), _i32(pages_used, "pages_used", (1,)),
+            _i32(cached_lens, "cached_lens", (batch,)), _i32(new_lens, "new_lens", (batch,)),
+            _i32(free_pages, "free_pages", (free_pages.numel(),)), batch, max_pages, page_size, free_pages.numel(),
+            n_rows, _stream_on(device, stream))
+    if st != 0:
+        raise QmmError(st, "qmm_paged_extend")
+    return seq_lens, slots, positions, pages_used
+
+
+def kv_append(cache: KVCache, k, v, slots, stream=None):
+    """Writes new keys and values (float32 [n, n_kv, head_dim], or [n, n_kv*head_dim]; rows any
+    stride apart, as views of a fused projection's output) into their slots (int32 [n]; a slot
+    outside the cache, such as -1, is skipped; the others must differ)."""
+    lib = load()
+    n = slots.shape[0]
+    row = cache.n_kv * cache.head_dim
+    _same_device(cache.k, k, v, slots)
+    with _On(cache.device):
+        st = lib.qmm_kv_append(cache._ptr, *_f32_rows(k, "k", n, row, cache.n_kv),
+                               *_f32_rows(v, "v", n, row, cache.n_kv), _i32(slots, "slots", (n,)), n,
+                               _stream_on(cache.device, stream))
+    if st != 0:
+        raise QmmError(st, "qmm_kv_append")
+
+
+def paged_attention_workspace_bytes(batch: int, n_q: int, cache: KVCache, max_pages: int) -> int:
+    """Bytes of workspace paged_attention uses for these sizes (0: none)."""
+    with _On(cache.device):
+        r = load().qmm_paged_attention_workspace_bytes(batch, n_q, cache.n_kv, cache.head_dim, max_pages, cache.page_size)
+    if r < 0:
+        raise QmmError(-r, "qmm_paged_attention_workspace_bytes")
+    return r
+
+
+def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=None, lse=None, workspace="auto",
+                    stream=None):
+    """Attention of one new token per sequence over its cached tokens; returns out (float32, q's
+    shape).  q: float32 [batch, n_q, head_dim] or [batch, n_q*head_dim], rows any stride apart;
+    block_table: int32 [batch, max_pages]; seq_lens: int32 [batch], the new token included, 0 for
+    a padded row (its output is zero).  scale: 1/sqrt(head_dim) by default.  lse: a float32
+    [batch, n_q] tensor that takes the log-sum-exp of the scores.  workspace: "auto" (allocated
+    for the call, from the graph's own memory under capture) or a device tensor of at least
+    paged_attention_workspace_bytes() bytes that no other call uses at the same time."""
+    import torch
+    lib = load()
+    batch = seq_lens.shape[0]
+    d = cache.head_dim
+    n_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
+    qp, ldq = _f32_rows(q, "q", batch, n_q * d, n_q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    op, ldo = _f32_rows(out, "out", batch, n_q * d, n_q)
+    table, max_pages, table_stride = _table(block_table, batch)
+    lp = None
+    if lse is not None:
+        lp = _dev(lse, "lse", torch.float32)
+        if lse.shape != (batch, n_q):
+            raise ValueError(f"lse must be [{batch}, {n_q}]")
+        _same_device(q, lse)
+    _same_device(cache.k, q, out, block_table, seq_lens)
+    device = cache.device
+    with _On(device):
+        nbytes = lib.qmm_paged_attention_workspace_bytes(batch, n_q, cache.n_kv, d, max_pages, cache.page_size)
+        ws, ws_len = None, 0
+        if nbytes > 0:
+            if isinstance(workspace, str):
+                if workspace != "auto":
+                    raise ValueError("workspace must be 'auto' or a tensor")
+                if stream is None:
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                else:
+                    # memory of the stream that uses it
+                    with torch.cuda.stream(stream):
+                        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            if workspace is not None:
+                _same_device(q, workspace)
+                ws, ws_len = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        st = lib.qmm_paged_attention(op, ldo, lp, qp, ldq, cache._ptr, table, table_stride,
+                                     _i32(seq_lens, "seq_lens", (batch,)), batch, n_q, max_pages,
+                                     d ** -0.5 if scale is None else scale, ws, ws_len, _stream_on(device, stream))
+    if st != 0:
+        raise QmmError(st, "qmm_paged_attention")
+    return out
+
+
+def _norm_rows(x, weight, residual, h):
+    """The arguments that both norms share: h's, x's and residual's pointers and strides, weight's
+    pointer, n, k."""
+    import torch
+    n, k = x.shape
+    xp, ldx = _f32_rows(x, "x", n, k)
+    rp, ldr = (None, 0) if residual is None else _f32_rows(residual, "residual", n, k)
+    hp, ldh = (None, 0) if h is None else _f32_rows(h, "h", n, k)
+    if weight.shape != (k,):
+        raise ValueError(f"weight must be [{k}]")
+    _same_device(x, weight, *(t for t in (residual, h) if t is not None))
+    return hp, ldh, xp, ldx, rp, ldr, _dev(weight, "weight", torch.float32), n, k
+
+
+def add_rmsnorm(x, weight, residual=None, eps: float = 1e-5, y=None, h=None, stream=None):
+    """Residual addition and RMS norm; returns (y, h): h = x + residual (None without a residual,
+    unless a tensor is given for it) and y = h * weight / sqrt(mean(h*h) + eps), float32 [n, k],
+    k a multiple of 4.  Rows of any of them may be any multiple of 4 apart."""
+    import torch
+    lib = load()
+    if y is None:
+        y = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+    if h is None and residual is not None:
+        h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+    args = _norm_rows(x, weight, residual, h)
+    yp, ldy = _f32_rows(y, "y", *x.shape)
+    device = _same_device(x, y)
+    with _On(device):
+        st = lib.qmm_add_rmsnorm(yp, ldy, *args, eps, _stream_on(device, stream))
+    if st != 0:
+        raise QmmError(st, "qmm_add_rmsnorm")
+    return y, h
+
+
+def add_rmsnorm_q8(x, weight, residual=None, eps: float = 1e-5, q=None, d=None, h=None, stream=None):
+    """add_rmsnorm with y as Q8_1 activations; returns (q int8 [n, k], d float32 [n, k/32], h), q
+    and d as moe_gateup_q8 takes them.  k a multiple of 32."""
+    import torch
+    lib = load()
+    n, k = x.shape
+    if q is None:
+        q = torch.empty((n, k), dtype=torch.int8, device=x.device)
+    if d is None:
+        d = torch.empty((n, k // 32), dtype=torch.float32, device=x.device)
+    if h is None and residual is not None:
+        h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+    if q.shape != (n, k) or d.shape != (n, k // 32):
+        raise ValueError(f"q must be [{n}, {k}] and d [{n}, {k // 32}]")
+    args = _norm_rows(x, weight, residual, h)
+    device = _same_device(x, q, d)
+    with _On(device):
+        st = lib.qmm_add_rmsnorm_q8(_dev(q, "q", torch.int8), _dev(d, "d", torch.float32), *args, eps,
+                                    _stream_on(device, stream))
+    if st != 0:
+        raise QmmError(st, "qmm_add_rmsnorm_q8")
+    return q, d, h

@@ -1,0 +1,683 @@
+// Attention of one new token per sequence over a paged key-value cache.
+//
+// For query head h of sequence b, over the sequence's cached tokens t:
+//     s_t = scale * q . k_t,  M = max s_t,  p_t = exp(s_t - M),
+//     out = sum p_t v_t / sum p_t,  lse = M + log(sum p_t)
+// in one pass over the cache with a running maximum (all exponentials are
+// powers of two: scale * log2(e) is folded into the scores).
+//
+// Bound.  Each cached row is read once for the whole group of query heads
+// that share it: 4 flops per element and query head on 2 (or 1) bytes, so
+// HBM bounds every group size the matrix cores keep up with.
+//
+// Precision.  q and out are f32, and the products are exact to f32: an f32
+// operand is split into f16 parts (high and low, 22 bits; for a bf16 cache
+// into three bf16 parts, 24 bits), each multiplied with the cache's own 16-bit
+// values on v_mfma_f32_16x16x32 into the same f32 sum.  The parts keep their
+// bits because q is scaled to [2^13, 2^14) per head and p to (0, 2^14], powers
+// of two that cancel at the end.  8-bit rows are exact as f16 codes; a key's
+// scale multiplies its score, a value's scale its probability.
+//
+// Tiles.  A wave takes 32 tokens at a time: scores as K q^T (two 16-token
+// tiles: lane (c, i) = (lane / 16, lane % 16) gets head i's scores of tokens
+// 4c..4c+3 and 16+4c..16+4c+3), then out^T += V^T p^T with exactly those eight
+// tokens as lane (c, i)'s k index, so neither p nor its running maximum ever
+// changes lanes.  K and V rows go from memory straight into registers, K in
+// operand layout; V's 16-bit transpose is one byte permute per operand dword.
+// Loads of the next tile are issued as soon as the present one's registers
+// are read, page ids one tile further ahead.
+//
+// Split.  All (head, sequence) units' tiles form one axis that is cut into
+// equal chunks, one per work group and a quarter of it per wave, whatever the
+// lengths are: every work group scans the lengths itself, so no host plan or
+// length is needed.  A unit inside one wave is finished there; parts of a unit
+// are joined in LDS, or, where it spans work groups, by a second kernel from
+// the workspace, always in token order, so results do not vary between calls.
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace qmm {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int TILE = 32;      // tokens per wave step
+constexpr int HEADS = 16;     // query heads per pass over a unit's rows
+constexpr float PBITS = 14.0f;
+constexpr float P_UNIT = 6.103515625e-05f;  // 2^-14
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float fbits(uint32_t u) { return __builtin_bit_cast(float, u); }
+__device__ __forceinline__ uint32_t ubits(float f) { return __builtin_bit_cast(uint32_t, f); }
+__device__ __forceinline__ float from_lane(float v, int lane) {
+    return fbits(__builtin_amdgcn_ds_bpermute(4 * lane, (int)ubits(v)));
+}
+
+// The maximum (sum) over the four lanes that differ in lane / 16.
+__device__ __forceinline__ float max_c(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum_c(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// Tokens of a sequence: -1 for a length the table cannot hold (its outputs
+// become NaN, nothing is read).
+__device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
+    const int n = a.lens[b];
+    return (n < 0 || n > a.capacity) ? -1 : n;
+}
+// A unit without tokens still takes one tile, whose wave writes its outputs.
+__device__ __forceinline__ int seq_tiles(int len) { return len <= TILE ? 1 : (len + TILE - 1) / TILE; }
+
+template <int N>
+__device__ __forceinline__ void ldg(uint32_t (&dst)[N], int at, const char* p, int bytes) {
+    if (bytes == 16) {
+        const u32x4 v = *(const u32x4*)p;
+        dst[at] = v.x; dst[at + 1] = v.y; dst[at + 2] = v.z; dst[at + 3] = v.w;
+    } else if (bytes == 8) {
+        const u32x2 v = *(const u32x2*)p;
+        dst[at] = v.x; dst[at + 1] = v.y;
+    } else if (bytes == 4) {
+        dst[at] = *(const uint32_t*)p;
+    } else {
+        dst[at] = *(const uint16_t*)p;
+    }
+}
+
+// Eight f32 as f16 (bf16) parts: x = part 0 + part 1 (+ part 2) up to 2^-22
+// (2^-24) of |x|.
+template <int KIND>
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&part)[KIND == KV_BF16 ? 3 : 2]) {
+    constexpr int NS = KIND == KV_BF16 ? 3 : 2;
+    float rest[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rest[j] = x[j];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        if constexpr (KIND == KV_BF16) {
+            bf16x8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = (__bf16)rest[j];
+                rest[j] -= (float)v[j];
+            }
+            part[s] = __builtin_bit_cast(u32x4, v);
+        } else {
+            f16x8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = (_Float16)rest[j];
+                rest[j] -= (float)v[j];
+            }
+            part[s] = __builtin_bit_cast(u32x4, v);
+        }
+    }
+}
+
+template <int KIND>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (KIND == KV_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Codes as f16.  A dword of codes with their sign bits flipped holds code +
+// 128 per byte; put under the byte 0x64 it is the f16 value 1024 + 128 + code.
+constexpr uint32_t SIGNS = 0x80808080u, B64 = 0x64646464u;
+__device__ __forceinline__ uint32_t codes2(uint32_t bytes, bool high) {
+    const uint32_t p = __builtin_amdgcn_perm(B64, bytes, high ? 0x04030402u : 0x04010400u);
+    const f16x2 v = __builtin_bit_cast(f16x2, p) - f16x2{(_Float16)1152.0f, (_Float16)1152.0f};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// One wave's state over a segment (some tiles of one unit), head i = lane % 16:
+// acc[o][r] belongs to the value dimension of operand o that lane 4c + r loads.
+template <int KIND, int NB>
+struct Segment {
+    static constexpr int D = 32 * NB;
+    static constexpr bool Q8 = KIND == KV_Q8;
+    static constexpr int NS = KIND == KV_BF16 ? 3 : 2;
+    static constexpr int ES = Q8 ? 1 : 2;          // bytes per element
+    static constexpr int KW = Q8 ? 2 * NB : 4 * NB;  // dwords of a lane's share of a key tile row
+    static constexpr int VW = Q8 ? (NB + 1) / 2 : NB;
+    // A value row is read by 16 lanes in runs of 8 elements per lane (128
+    // dimensions), then 4 (64) and 2 (32) as head_dim leaves them.
+    static constexpr int N8 = NB / 4;
+    static constexpr bool N4 = (NB & 2) != 0, N2 = (NB & 1) != 0;
+
+    f32x4 acc[2 * NB];
+    float m, l;
+    float vexp;      // 8-bit values: acc holds sums divided by this power of two
+
+    static __device__ __forceinline__ void load_k(uint32_t (&kr)[KW], const char* row, int c) {
+        if constexpr (Q8) {
+#pragma unroll
+            for (int p = 0; p < NB / 2; ++p) ldg(kr, 4 * p, row + 64 * p + 16 * c, 16);
+            if constexpr (N2) ldg(kr, 4 * (NB / 2), row + 64 * (NB / 2) + 8 * c, 8);
+        } else {
+#pragma unroll
+            for (int s = 0; s < NB; ++s) ldg(kr, 4 * s, row + 64 * s + 16 * c, 16);
+        }
+    }
+    static __device__ __forceinline__ void load_v(uint32_t (&vr)[VW], const char* row, int i) {
+#pragma unroll
+        for (int n = 0; n < N8; ++n) ldg(vr, n * 2 * ES, row + ES * (128 * n + 8 * i), 8 * ES);
+        if constexpr (N4) ldg(vr, N8 * 2 * ES, row + ES * (128 * N8 + 4 * i), 4 * ES);
+        if constexpr (N2) ldg(vr, (N8 * 2 + (N4 ? 1 : 0)) * ES, row + ES * (128 * N8 + (N4 ? 64 : 0) + 2 * i), 2 * ES);
+    }
+    // first dimension of the eight that lane c's share of step s holds
+    static __device__ __forceinline__ int kdim(int s, int c) {
+        if constexpr (Q8) {
+            if (N2 && s == NB - 1) return 32 * s + 8 * c;
+            return 64 * (s / 2) + 16 * c + 8 * (s % 2);
+        } else {
+            return 32 * s + 8 * c;
+        }
+    }
+    // the key operand of step s
+    static __device__ __forceinline__ u32x4 key(const uint32_t (&kr)[KW], int s) {
+        if constexpr (Q8) {
+            const uint32_t x = kr[2 * s] ^ SIGNS, y = kr[2 * s + 1] ^ SIGNS;
+            return u32x4{codes2(x, false), codes2(x, true), codes2(y, false), codes2(y, true)};
+        } else {
+            return u32x4{kr[4 * s], kr[4 * s + 1], kr[4 * s + 2], kr[4 * s + 3]};
+        }
+    }
+    // the value operand o: its element of the lane's eight rows
+    static __device__ __forceinline__ u32x4 value(const uint32_t (&vr)[8][VW], int o) {
+        uint32_t out[4];
+        if constexpr (Q8) {
+            const int w = o / 4, x = o % 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = __builtin_amdgcn_perm(vr[2 * j + 1][w] ^ SIGNS, vr[2 * j][w] ^ SIGNS,
+                                                           x < 2 ? 0x05010400u : 0x07030602u);
+                out[j] = codes2(two, x & 1);
+            }
+        } else {
+            const int w = o / 2;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                out[j] = __builtin_amdgcn_perm(vr[2 * j + 1][w], vr[2 * j][w], (o & 1) ? 0x07060302u : 0x05040100u);
+        }
+        return u32x4{out[0], out[1], out[2], out[3]};
+    }
+
+    // Tiles [t, t + n) of sequence b (len tokens) for `rows` heads from query head head0.
+    __device__ __forceinline__ void run(const AttnArgs& a, int b, int len, int kvh, int head0, int rows, int t, int n) {
+        const int lane = threadIdx.x & 63, c = lane >> 4, i = lane & 15;
+        m = -INFINITY;
+        l = 0.0f;
+        vexp = fbits(1u << 23);
+#pragma unroll
+        for (int o = 0; o < 2 * NB; ++o) acc[o] = f32x4{0, 0, 0, 0};
+        if (len <= 0) {
+            l = len < 0 ? NAN : 0.0f;
+            return;
+        }
+        const char* kb = (const char*)a.k + (int64_t)kvh * a.head_bytes;
+        const char* vb = (const char*)a.v + (int64_t)kvh * a.head_bytes;
+        const float* sb = Q8 ? ((lane & 32) ? a.v_scale : a.k_scale) + (int64_t)kvh * a.scale_head : nullptr;
+        const int* table = a.table + (int64_t)b * a.table_stride;
+        bool bad = false;
+
+        // page id of the lane's token (lane % 32) of tile tt; tokens behind the last read as the last
+        auto token = [&](int tt) {
+            const int tok = TILE * tt + (lane & 31);
+            return tok < len ? tok : len - 1;
+        };
+        auto page_id = [&](int tt) { return table[token(tt) >> a.page_log2]; };
+        uint32_t off;        // the row of the lane's token, in 16-byte units from the head's first
+        float sc = 0.0f;     // its key (lanes 0..31) or value scale
+        auto locate = [&](int id, int tt) {
+            const bool out = (uint32_t)id >= (uint32_t)a.n_pages;
+            bad |= out;
+            const uint32_t pg = out ? 0u : (uint32_t)id, slot = (uint32_t)token(tt) & (uint32_t)(a.page_size - 1);
+            off = pg * a.page_units + slot * a.slot_units;
+            if constexpr (Q8) sc = sb[(int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot];
+        };
+        auto row_of = [&](const char* base, int src) {
+            return base + ((uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(4 * src, (int)off) << 4);
+        };
+        uint32_t kr[2][KW], vr[8][VW];
+        auto load_keys = [&]() {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) load_k(kr[h], row_of(kb, 16 * h + i), c);
+        };
+        auto tok_of = [&](int j) { return (j < 4 ? 0 : 12) + 4 * c + j; };  // token of the lane's k index j
+        auto load_values = [&]() {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) load_v(vr[j], row_of(vb, tok_of(j)), i);
+        };
+
+        int id = page_id(t);
+        // the query heads, split; lanes past the last head hold zeros
+        u32x4 qp[NB][NS];
+        float qs;
+        {
+            const float* qrow = a.q + (int64_t)b * a.q_stride + (int64_t)(head0 + (i < rows ? i : 0)) * D;
+            float x[NB][8];
+            float top = 0.0f;
+#pragma unroll
+            for (int s = 0; s < NB; ++s) {
+                const f32x4 lo = *(const f32x4*)(qrow + kdim(s, c)), hi = *(const f32x4*)(qrow + kdim(s, c) + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[s][j] = i < rows ? lo[j] : 0.0f;
+                    x[s][4 + j] = i < rows ? hi[j] : 0.0f;
+                    top = fmaxf(top, fmaxf(fabsf(x[s][j]), fabsf(x[s][4 + j])));
+                }
+            }
+            locate(id, t);
+            load_keys();
+            if (n > 1) id = page_id(t + 1);
+            load_values();
+            top = max_c(top);
+            // exponent field of 2^(13 - floor(log2 top)), kept normal with its inverse
+            int e = 267 - (int)(ubits(top) >> 23);
+            e = e > 253 ? 253 : (e < 1 ? 1 : e);
+            const float f = fbits((uint32_t)e << 23);
+            qs = fbits((uint32_t)(254 - e) << 23) * a.scale_log2e;
+#pragma unroll
+            for (int s = 0; s < NB; ++s) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[s][j] *= f;
+                split8<KIND>(x[s], qp[s]);
+            }
+        }
+
+        for (int it = 0; it < n; ++it) {
+            const int tt = t + it;
+            const bool more = it + 1 < n;
+            f32x4 s4[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+            for (int s = 0; s < NB; ++s)
+#pragma unroll
+                for (int p = 0; p < NS; ++p)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) s4[h] = mfma<KIND>(key(kr[h], s), qp[s][p], s4[h]);
+            float s[8], vs[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[j] = s4[j / 4][j % 4] * qs;
+                if constexpr (Q8) {
+                    s[j] *= from_lane(sc, tok_of(j));
+                    vs[j] = from_lane(sc, 32 + tok_of(j));
+                }
+            }
+            if (TILE * (tt + 1) > len) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (TILE * tt + tok_of(j) >= len) s[j] = -INFINITY;
+            }
+            if (more) {
+                locate(id, tt + 1);
+                load_keys();
+                if (it + 2 < n) id = page_id(tt + 2);
+            }
+            float top = s[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = fmaxf(top, s[j]);
+            top = fmaxf(m, max_c(top));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float alpha = __builtin_amdgcn_exp2f(m - base);
+            m = top;
+            float p[8], sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                p[j] = __builtin_amdgcn_exp2f(s[j] - base + PBITS);
+                sum += p[j];
+            }
+            l = l * alpha + sum;
+            if constexpr (Q8) {
+                // value scales relative to the largest so far, rounded up to a power of two
+                float big = vs[0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) big = fmaxf(big, fabsf(vs[j]));
+                big = max_c(fabsf(big));
+                int e = (int)(ubits(big) >> 23) + 1;
+                e = e < 2 ? 2 : (e > 253 ? 253 : e);
+                const float v2 = fmaxf(vexp, fbits((uint32_t)e << 23));
+                alpha *= vexp * fbits((254u << 23) - ubits(v2));
+                vexp = v2;
+                const float inv = fbits((254u << 23) - ubits(v2));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    p[j] *= vs[j] * inv;
+                    // The product as one f32 value: the compiler otherwise rounds it to f16 for the
+                    // high part straight from its factors (v_fma_mixlo_f16), which near a tie is not
+                    // the f16 that the low part was taken against (2^-11 off, seen about once in 10^4).
+                    asm("" : "+v"(p[j]));
+                }
+            }
+            if (__any(alpha != 1.0f)) {
+#pragma unroll
+                for (int o = 0; o < 2 * NB; ++o) acc[o] *= alpha;
+            }
+            u32x4 pp[NS];
+            split8<KIND>(p, pp);
+#pragma unroll
+            for (int o = 0; o < 2 * NB; ++o) {
+                const u32x4 v = value(vr, o);
+#pragma unroll
+                for (int q = 0; q < NS; ++q) acc[o] = mfma<KIND>(v, pp[q], acc[o]);
+            }
+            if (more) load_values();
+        }
+        if (__any(bad)) l = NAN;
+        l = sum_c(l);
+        if constexpr (Q8) {
+#pragma unroll
+            for (int o = 0; o < 2 * NB; ++o) acc[o] *= vexp;
+        }
+    }
+
+    // f(dimension, the sums of it and the next one or three, times w) over the lane's sums
+    template <typename F>
+    __device__ __forceinline__ void each(float w, F f) const {
+        const int rho = 4 * ((threadIdx.x >> 4) & 3);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+#pragma unroll
+            for (int o = 0; o < 8 * N8; o += 4)
+                f(128 * (o / 8) + 8 * (rho + r) + o % 8,
+                  f32x4{acc[o][r] * w, acc[o + 1][r] * w, acc[o + 2][r] * w, acc[o + 3][r] * w});
+            if constexpr (N4) {
+                constexpr int o = 8 * N8;
+                f(128 * N8 + 4 * (rho + r), f32x4{acc[o][r] * w, acc[o + 1][r] * w, acc[o + 2][r] * w, acc[o + 3][r] * w});
+            }
+            if constexpr (N2) {
+                constexpr int o = 2 * NB - 2;
+                f(D - 32 + 2 * (rho + r), f32x2{acc[o][r] * w, acc[o + 1][r] * w});
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + __builtin_amdgcn_logf(l * P_UNIT)) * LN2; }
+
+// A unit: (kv head, block of at most HEADS of its query heads, sequence).
+struct Unit {
+    int b, kvh, head0, rows;
+};
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int hs, int b) {
+    Unit u;
+    u.b = b;
+    u.kvh = hs / a.blocks_per_kv;
+    const int blk = hs - u.kvh * a.blocks_per_kv;
+    u.head0 = u.kvh * a.group + blk * a.heads_per_block;
+    u.rows = a.group - blk * a.heads_per_block;
+    if (u.rows > a.heads_per_block) u.rows = a.heads_per_block;
+    return u;
+}
+
+// A part: heads_per_block rows of D sums, then (m, l) per row, in whole 16-byte units.
+__host__ __device__ __forceinline__ int part_floats(int heads_per_block, int d) {
+    return heads_per_block * d + ((2 * heads_per_block + 3) & ~3);
+}
+
+// Floor of x / y for 0 <= x < 2^53, 0 < y: a quotient just below a whole
+// number is at least 1/x below it, so rounding to 53 bits does not reach it.
+__device__ __forceinline__ int64_t floor_div(int64_t x, int64_t y) { return (int64_t)((double)x / (double)y); }
+
+template <int KIND, int NB>
+__global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void paged_attn_kernel(const AttnArgs a) {
+    constexpr int D = 32 * NB;
+    extern __shared__ __attribute__((aligned(16))) float parts[];  // [wave][2] parts
+    __shared__ int wsum[4];
+    __shared__ int start_hs[4], start_b[4], start_t[4];
+    __shared__ int part_unit[4][2], part_ends[4][2], part_follow[4];
+    const int tid = threadIdx.x, w = uni(tid >> 6), lane = tid & 63;
+    const int g = blockIdx.x;
+
+    // tiles per head space: each thread counts a run of consecutive sequences
+    const int per = (a.batch + 255) / 256;
+    const int b_lo = tid * per, b_hi = b_lo + per < a.batch ? b_lo + per : a.batch;
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += seq_tiles(seq_len(a, b));
+    int incl = mine;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const int v = __shfl_up(incl, s);
+        if (lane >= s) incl += v;
+    }
+    if (lane == 63) wsum[w] = incl;
+    if (tid < 8) part_unit[tid >> 1][tid & 1] = -1;
+    __syncthreads();
+    int before = incl - mine, total = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (i < w) before += wsum[i];
+        total += wsum[i];
+    }
+    total = uni(total);
+    const int64_t all = (int64_t)total * a.head_spaces;
+    int64_t chunk = floor_div(all + a.groups - 1, a.groups);
+    chunk = (chunk + 3) & ~(int64_t)3;  // at least a tile per wave
+    const int64_t lo = g * chunk, hi = lo + chunk < all ? lo + chunk : all;
+    if (lo >= all) {
+        if (tid == 0 && a.meta) a.meta[g] = make_int2(0, 0);
+        return;
+    }
+    const int64_t wc = chunk >> 2;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t x = lo + i * wc;
+        if (x >= hi) break;
+        const int hs = (int)floor_div(x, total), r = (int)(x - (int64_t)hs * total);
+        if (r >= before && r < before + mine) {
+            int at = before, b = b_lo;
+            for (;; ++b) {
+                const int nt = seq_tiles(seq_len(a, b));
+                if (r < at + nt) break;
+                at += nt;
+            }
+            start_hs[i] = hs;
+            start_b[i] = b;
+            start_t[i] = r - at;
+        }
+    }
+    __syncthreads();
+
+    const int pf = part_floats(a.heads_per_block, D);
+    int64_t pos = lo + w * wc;
+    const int64_t end = pos + wc < hi ? pos + wc : hi;
+    if (pos < end) {
+        int hs = uni(start_hs[w]), b = uni(start_b[w]), t = uni(start_t[w]);
+        while (pos < end) {
+            const int len = uni(seq_len(a, b)), nt = seq_tiles(len);
+            const int n = (int)(nt - t < end - pos ? nt - t : end - pos);
+            const Unit u = unit_of(a, hs, b);
+            Segment<KIND, NB> seg;
+            seg.run(a, b, len, u.kvh, u.head0, u.rows, t, n);
+            const int i = lane & 15;
+            if (n == nt) {  // the whole unit: its outputs
+                if (i < u.rows) {
+                    const float inv = len == 0 ? 0.0f : 1.0f / seg.l;
+                    float* o = a.out + (int64_t)b * a.out_stride + (int64_t)(u.head0 + i) * D;
+                    seg.each(inv, [&](int d, auto v) { *(decltype(v)*)(o + d) = v; });
+                    if (a.lse && lane < 16)
+                        a.lse[(int64_t)b * a.n_q + u.head0 + i] = len == 0 ? -INFINITY : lse_of(seg.m, seg.l);
+                }
+            } else {
+                const int slot = t == 0 ? 1 : 0;
+                float* o = parts + (w * 2 + slot) * pf;
+                if (i < a.heads_per_block) {
+                    float* row = o + i * D;
+                    seg.each(1.0f, [&](int d, auto v) { *(decltype(v)*)(row + d) = v; });
+                    if (lane < 16) {
+                        o[a.heads_per_block * D + 2 * i] = seg.m;
+                        o[a.heads_per_block * D + 2 * i + 1] = seg.l;
+                    }
+                }
+                if (lane == 0) {
+                    part_unit[w][slot] = hs * a.batch + b;
+                    part_ends[w][slot] = t + n == nt;
+                    if (slot) part_follow[w] = (int)floor_div(pos + nt - 1, chunk) - g;
+                }
+            }
+            pos += n;
+            t = 0;
+            if (++b == a.batch) {
+                b = 0;
+                ++hs;
+            }
+        }
+    }
+    __syncthreads();
+
+    // Join the parts of each unit, in token order: a unit that starts here
+    // (slot 1 of some wave) or came in from the previous work group (slot 0 of
+    // wave 0), and the slots 0 of the following waves up to its end.
+    int2 info = make_int2(0, 0);
+    for (int first = -1; first < 4; ++first) {
+        const int w0 = first < 0 ? 0 : first, s0 = first < 0 ? 0 : 1;
+        const int unit = part_unit[w0][s0];
+        if (unit < 0) continue;
+        int last = w0;
+        bool ends = part_ends[w0][s0];
+        while (!ends && last < 3 && part_unit[last + 1][0] == unit) ends = part_ends[++last][0];
+        const Unit u = unit_of(a, unit / a.batch, unit % a.batch);
+        const bool whole = s0 == 1 && ends;
+        float* ws = whole ? nullptr : a.parts + (int64_t)(2 * g + s0) * pf;
+        if (s0 == 1 && !ends) info = make_int2(unit + 1, part_follow[w0]);
+        for (int x = tid; x < u.rows * (D / 4); x += 256) {
+            const int row = x / (D / 4), d = 4 * (x % (D / 4));
+            const float* ml = parts + a.heads_per_block * D + 2 * row;
+            float top = -INFINITY;
+            for (int v = w0; v <= last; ++v) top = fmaxf(top, ml[(v * 2 + (v == w0 ? s0 : 0)) * pf]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            f32x4 o = {0, 0, 0, 0};
+            float l = 0.0f;
+            for (int v = w0; v <= last; ++v) {
+                const int at = (v * 2 + (v == w0 ? s0 : 0)) * pf;
+                const float f = __builtin_amdgcn_exp2f(ml[at] - base);
+                o += *(const f32x4*)(parts + at + row * D + d) * f;
+                l += ml[at + 1] * f;
+            }
+            if (whole) {
+                *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * D + d) = o * (1.0f / l);
+                if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l);
+            } else {
+                *(f32x4*)(ws + row * D + d) = o;
+                if (d == 0) {
+                    ws[a.heads_per_block * D + 2 * row] = top;
+                    ws[a.heads_per_block * D + 2 * row + 1] = l;
+                }
+            }
+        }
+    }
+    if (tid == 0 && a.meta) a.meta[g] = info;
+}
+
+// The units that span work groups.  A work group's last unit may continue in
+// the following ones (meta: its number + 1, and how many); its parts are part
+// 1 of that work group and part 0 of the others.  One work group of this
+// kernel per such unit and query head: threads take (part, four dimensions),
+// parts a thread group apart, then the thread groups' sums are added in order.
+template <int D>
+__global__ __launch_bounds__(256) void paged_attn_join_kernel(const AttnArgs a) {
+    constexpr int DL = D / 4, PG = 256 / DL;
+    __shared__ f32x4 sums[PG][DL];
+    __shared__ float pm[PG], pl[PG];
+    const int g = blockIdx.x, row = blockIdx.y;
+    const int2 info = a.meta[g];
+    if (info.y == 0) return;
+    const int unit = info.x - 1, n = info.y + 1;
+    const Unit u = unit_of(a, unit / a.batch, unit % a.batch);
+    if (row >= u.rows) return;
+    const int pf = part_floats(a.heads_per_block, D);
+    const int tid = threadIdx.x, pg = tid / DL, d = 4 * (tid % DL);
+    auto part = [&](int p) { return a.parts + (int64_t)(2 * (g + p) + (p == 0 ? 1 : 0)) * pf; };
+    if (pg < PG) {
+        f32x4 o = {0, 0, 0, 0};
+        float m = -INFINITY, l = 0.0f;
+        for (int p = pg; p < n; p += PG) {
+            const float* at = part(p);
+            const f32x4 v = *(const f32x4*)(at + row * D + d);
+            const float m2 = at[a.heads_per_block * D + 2 * row], l2 = at[a.heads_per_block * D + 2 * row + 1];
+            const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.0f : top;
+            const float f = __builtin_amdgcn_exp2f(m - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
+            o = o * f + v * f2;
+            l = l * f + l2 * f2;
+            m = top;
+        }
+        sums[pg][tid % DL] = o;
+        if (d == 0) {
+            pm[pg] = m;
+            pl[pg] = l;
+        }
+    }
+    __syncthreads();
+    if (tid >= DL) return;
+    float top = -INFINITY;
+    for (int p = 0; p < PG; ++p) top = fmaxf(top, pm[p]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    f32x4 o = {0, 0, 0, 0};
+    float l = 0.0f;
+    for (int p = 0; p < PG; ++p) {
+        const float f = __builtin_amdgcn_exp2f(pm[p] - base);
+        o += sums[p][tid] * f;
+        l += pl[p] * f;
+    }
+    *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * D + d) = o * (1.0f / l);
+    if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l);
+}
+
+template <int KIND, int NB>
+void launch(const AttnArgs& a, hipStream_t st) {
+    const size_t lds = (size_t)8 * part_floats(a.heads_per_block, 32 * NB) * sizeof(float);
+    if (lds > 64 * 1024)
+        (void)hipFuncSetAttribute((const void*)paged_attn_kernel<KIND, NB>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    paged_attn_kernel<KIND, NB><<<dim3((unsigned)a.groups), 256, lds, st>>>(a);
+    if (a.groups > 1)
+        paged_attn_join_kernel<32 * NB><<<dim3((unsigned)a.groups, (unsigned)a.heads_per_block), 256, 0, st>>>(a);
+}
+
+template <int KIND>
+void launch_kind(const AttnArgs& a, int head_dim, hipStream_t st) {
+    switch (head_dim / 32) {
+        case 1: launch<KIND, 1>(a, st); break;
+        case 2: launch<KIND, 2>(a, st); break;
+        case 3: launch<KIND, 3>(a, st); break;
+        case 4: launch<KIND, 4>(a, st); break;
+        case 5: launch<KIND, 5>(a, st); break;
+        case 6: launch<KIND, 6>(a, st); break;
+        case 7: launch<KIND, 7>(a, st); break;
+        case 8: launch<KIND, 8>(a, st); break;
+    }
+}
+
+}  // namespace
+
+AttnPlan plan_paged_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t head_dim, int64_t capacity, int num_cu) {
+    AttnPlan p;
+    const int64_t group = n_q / n_kv;
+    p.blocks_per_kv = (int)((group + HEADS - 1) / HEADS);
+    p.heads_per_block = (int)((group + p.blocks_per_kv - 1) / p.blocks_per_kv);
+    p.head_spaces = n_kv * p.blocks_per_kv;
+    // work groups: two per CU, or as many as the tables' tiles give a tile per wave
+    const int64_t tiles = (capacity + TILE - 1) / TILE;
+    const int64_t most = (batch * tiles * p.head_spaces + 3) / 4;
+    const int64_t want = (int64_t)num_cu * 2;
+    p.groups = (int)(most < want ? most : want);
+    p.meta_bytes = ((int64_t)p.groups * 8 + 255) / 256 * 256;
+    const int64_t part = (int64_t)part_floats(p.heads_per_block, (int)head_dim) * 4;
+    p.ws_bytes = p.groups > 1 ? p.meta_bytes + (2 * p.groups * part + 255) / 256 * 256 : 0;
+    return p;
+}
+
+void launch_paged_attention(const AttnArgs& a, int kind, int head_dim, hipStream_t st) {
+    if (kind == KV_F16)
+        launch_kind<KV_F16>(a, head_dim, st);
+    else if (kind == KV_BF16)
+        launch_kind<KV_BF16>(a, head_dim, st);
+    else
+        launch_kind<KV_Q8>(a, head_dim, st);
+}
+
+}  // namespace qmm

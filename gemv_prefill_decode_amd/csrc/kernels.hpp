@@ -172,4 +172,78 @@ constexpr int MFMA_BM = 128;
 constexpr int MFMA_BN = 128;
 constexpr int MFMA_BM_MAX = 256;
 
+// Key-value cache kinds (qmm_kv_kind).
+enum : int { KV_F16 = 0, KV_BF16 = 1, KV_Q8 = 2 };
+
+// Page tables of a step: the pages each sequence newly needs, taken from
+// free_pages in sequence order, and the new tokens' slots and positions.
+struct ExtendArgs {
+    int* table;
+    int64_t table_stride;
+    int *seq_lens, *slots, *positions, *pages_used;
+    const int *cached, *fresh, *free_pages;
+    int batch, page_log2, n_free, n_rows;
+    int64_t capacity;  // tokens a table row holds
+};
+void launch_paged_extend(const ExtendArgs& a, hipStream_t st);
+
+// New rows into their slots of the cache; strides of the cache in elements.
+struct AppendArgs {
+    void *kc, *vc;
+    float *ks, *vs;
+    const float *k, *v;
+    int64_t k_stride, v_stride;  // floats between tokens
+    const int* slots;
+    int64_t n;
+    int n_kv, n_slots, page_log2;
+    int64_t page_stride, head_stride, slot_stride;
+    int64_t scale_page, scale_head, scale_slot;
+};
+void launch_kv_append(const AppendArgs& a, int kind, int head_dim, hipStream_t st);
+
+// Paged attention.  A head space is a kv head and a block of at most 16 of
+// the query heads that share it; groups work groups each take an equal run of
+// (head space, sequence, tile).
+struct AttnPlan {
+    int blocks_per_kv, heads_per_block, groups;
+    int64_t head_spaces;
+    int64_t meta_bytes, ws_bytes;  // workspace: meta, then two parts per group
+};
+AttnPlan plan_paged_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t head_dim, int64_t capacity, int num_cu);
+struct AttnArgs {
+    float *out, *lse;
+    const float* q;
+    int64_t out_stride, q_stride;  // floats between sequences
+    const void *k, *v;
+    const float *k_scale, *v_scale;
+    int64_t head_bytes;            // between kv heads
+    uint32_t page_units, slot_units;  // strides in 16-byte units
+    int64_t scale_page, scale_head, scale_slot;
+    int n_pages, page_log2, page_size;
+    const int* table;
+    int64_t table_stride;
+    const int* lens;
+    int batch, n_q, group, capacity;
+    int blocks_per_kv, heads_per_block, groups;
+    int64_t head_spaces;
+    float scale_log2e;
+    int2* meta;
+    float* parts;
+};
+void launch_paged_attention(const AttnArgs& a, int kind, int head_dim, hipStream_t st);
+
+// Residual addition and RMS norm of n rows of k; y (f32) or q and d (Q8_1).
+struct NormArgs {
+    float* y;
+    int8_t* q;
+    float* d;
+    float* h;
+    const float *x, *r, *w;
+    int64_t y_stride, h_stride, x_stride, r_stride;
+    int64_t n;
+    int k;
+    float eps, inv_k;
+};
+void launch_add_rmsnorm(const NormArgs& a, hipStream_t st);
+
 }  // namespace qmm

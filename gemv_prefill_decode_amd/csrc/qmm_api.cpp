@@ -167,10 +167,8 @@ MfmaForceState parse_force() {
     return g_force;
 }
 
-// Tuning for the current device; false if a tuning variable is malformed.
-bool gemv_tuning(qmm::GemvTuning* t) {
-    std::call_once(g_tune_once, parse_tune);
-    if (g_tune.bad) return false;
+// Properties of the current device, read once per device.
+DevProps dev_props() {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) dev = 0;
     DevProps p;
@@ -190,6 +188,14 @@ bool gemv_tuning(qmm::GemvTuning* t) {
         std::lock_guard<std::mutex> lk(g_cu_mu);
         if (dev >= 0 && dev < 64) g_dev[dev] = p;
     }
+    return p;
+}
+
+// Tuning for the current device; false if a tuning variable is malformed.
+bool gemv_tuning(qmm::GemvTuning* t) {
+    std::call_once(g_tune_once, parse_tune);
+    if (g_tune.bad) return false;
+    const DevProps p = dev_props();
     t->num_cu = p.cu;
     t->lds_per_wg = p.lds_wg;
     t->lds_per_cu = p.lds_cu;
@@ -308,6 +314,117 @@ int gemm_impl(float* dst, int64_t ldd, const void* w, const float* x, int64_t ld
     }
     qmm::launch_gemm_mfma(dst, w, x, m, k, n, qtype, rb, pl, ws, ldx, ldd, stream);
     return launch_status();
+}
+
+// ------------------------------------------------------------------ decode step
+// Tokens of a cache or a table row, table entries and rows of a step: int32
+// with room for the kernels' strides and tiles past the last.
+constexpr int64_t KV_TOKENS_MAX = (int64_t)1 << 30;
+
+int log2_of(int64_t pow2) {
+    int n = 0;
+    while (((int64_t)1 << n) < pow2) ++n;
+    return n;
+}
+
+struct KvExtent {
+    int64_t bytes, scale_bytes;  // of k (and of v); of each scale array
+};
+
+// Last element of [pages][heads][slots] with these strides, plus one row;
+// -1 if it passes int64.
+int64_t strided_extent(const qmm_kv_cache* c, int64_t sp, int64_t sh, int64_t ss, int64_t row) {
+    int64_t p, h, s;
+    if (!mul_ok(c->n_pages - 1, sp, &p) || !mul_ok(c->n_kv - 1, sh, &h) || !mul_ok(c->page_size - 1, ss, &s)) return -1;
+    const int64_t lim = INT64_MAX / 8;
+    if (p > lim || h > lim || s > lim) return -1;
+    return p + h + s + row;
+}
+
+int check_cache(const qmm_kv_cache* c, KvExtent* e) {
+    if (!c || !c->k || !c->v) return QMM_ERR_NULL;
+    if (c->kind != QMM_KV_F16 && c->kind != QMM_KV_BF16 && c->kind != QMM_KV_Q8) return QMM_ERR_QTYPE;
+    const bool q8 = c->kind == QMM_KV_Q8;
+    if (q8 && (!c->k_scale || !c->v_scale)) return QMM_ERR_NULL;
+    if (c->n_pages < 1 || c->n_kv < 1 || c->page_size < 1 || c->head_dim < 1 ||
+        (c->page_size & (c->page_size - 1)) != 0)
+        return QMM_ERR_SHAPE;
+    if (c->head_dim % 32 != 0) return QMM_ERR_K_ALIGN;
+    if (c->head_dim > 256) return QMM_ERR_RANGE;
+    const int64_t unit = q8 ? 16 : 8;  // elements in 16 bytes
+    for (const int64_t s : {c->page_stride, c->head_stride, c->slot_stride}) {
+        if (s < c->head_dim) return QMM_ERR_SHAPE;
+        if (s % unit != 0) return QMM_ERR_ALIGN;
+    }
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QMM_ERR_ALIGN;
+    int64_t tokens;
+    if (!mul_ok(c->n_pages, c->page_size, &tokens) || tokens > KV_TOKENS_MAX || c->n_kv > 65535) return QMM_ERR_RANGE;
+    const int64_t elems = strided_extent(c, c->page_stride, c->head_stride, c->slot_stride, c->head_dim);
+    // rows are addressed by a 32-bit count of 16-byte units from a head's first row
+    if (elems < 0 || elems / unit >= ((int64_t)1 << 32)) return QMM_ERR_RANGE;
+    e->bytes = elems * (q8 ? 1 : 2);
+    e->scale_bytes = 0;
+    if (q8) {
+        for (const int64_t s : {c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride})
+            if (s < 1) return QMM_ERR_SHAPE;
+        if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return QMM_ERR_ALIGN;
+        const int64_t sc = strided_extent(c, c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride, 1);
+        if (sc < 0 || sc >= ((int64_t)1 << 40)) return QMM_ERR_RANGE;
+        e->scale_bytes = sc * 4;
+    }
+    return QMM_OK;
+}
+
+// Sizes of a paged attention; *cap: tokens a table row holds.
+int check_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t head_dim, int64_t max_pages, int64_t page_size,
+                    int64_t* cap) {
+    if (batch < 1 || n_q < 1 || n_kv < 1 || max_pages < 1 || head_dim < 1 || page_size < 1 || n_q % n_kv != 0 ||
+        (page_size & (page_size - 1)) != 0)
+        return QMM_ERR_SHAPE;
+    if (head_dim % 32 != 0) return QMM_ERR_K_ALIGN;
+    if (head_dim > 256 || batch > (1 << 20) || n_q > 65535 || !mul_ok(max_pages, page_size, cap) || *cap > KV_TOKENS_MAX)
+        return QMM_ERR_RANGE;
+    // (head space, sequence) numbers and a head space's tiles are int32
+    if (batch * n_q > INT_MAX - 1 || batch * ((*cap + 31) / 32) > INT_MAX) return QMM_ERR_RANGE;
+    return QMM_OK;
+}
+
+// The checks that both outputs of the norm share, and its arguments.  unit: k
+// must be a multiple; y (a->y) has rows ldy apart, q and d are packed.
+int norm_args(qmm::NormArgs* a, float* h, int64_t ldh, const float* x, int64_t ldx, const float* r, int64_t ldr,
+              const float* w, int64_t n, int64_t k, float eps, int64_t unit, int64_t ldy) {
+    if (!x || !w) return QMM_ERR_NULL;
+    if (n < 1 || k < 1 || ldx < k || (r && ldr < k) || (h && ldh < k)) return QMM_ERR_SHAPE;
+    if (k % unit != 0) return QMM_ERR_K_ALIGN;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(r, 16) || !aligned(h, 16) || ldx % 4 != 0 || (r && ldr % 4 != 0) ||
+        (h && ldh % 4 != 0))
+        return QMM_ERR_ALIGN;
+    if (k > (1 << 24) || n > INT_MAX) return QMM_ERR_RANGE;  // a row per work group; exact float(k)
+    if (!(eps >= 0.0f) || eps - eps != 0.0f) return QMM_ERR_RANGE;
+    int64_t t;
+    const int64_t strides[] = {ldx, r ? ldr : k, h ? ldh : k, a->y ? ldy : k};
+    for (const int64_t s : strides)
+        if (!mul_ok(n, s, &t) || t > INT64_MAX / 4) return QMM_ERR_SHAPE;
+    auto span = [&](const float* p, int64_t ld) { return Span{p, p ? ((n - 1) * ld + k) * 4 : 0}; };
+    const Span ins[] = {span(x, ldx), span(r, ldr), {w, k * 4}};
+    const Span outs[] = {span(a->y, ldy), {a->q, a->q ? n * k : 0}, {a->d, a->d ? n * k / 8 : 0}, span(h, ldh)};
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps_any(outs[i].p, outs[i].n, {ins[0], ins[1], ins[2]})) return QMM_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QMM_ERR_ALIAS;
+    }
+    a->h = h;
+    a->h_stride = ldh;
+    a->x = x;
+    a->x_stride = ldx;
+    a->r = r;
+    a->r_stride = ldr;
+    a->w = w;
+    a->n = n;
+    a->k = (int)k;
+    a->eps = eps;
+    a->inv_k = 1.0f / (float)k;
+    return QMM_OK;
 }
 
 }  // namespace
@@ -693,6 +810,174 @@ int qmm_stream_loadonly(uint32_t* sink, const void* w, int64_t m, int64_t k, int
     qmm::GemvTuning tune;
     if (!gemv_tuning(&tune)) return QMM_ERR_RANGE;
     qmm::launch_loadonly(sink, w, m, k, qtype, rb, tune, stream);
+    return launch_status();
+}
+
+int qmm_paged_extend(int32_t* block_table, int64_t table_stride, int32_t* seq_lens, int32_t* slots,
+                     int32_t* positions, int32_t* pages_used, const int32_t* cached_lens, const int32_t* new_lens,
+                     const int32_t* free_pages, int64_t batch, int64_t max_pages, int64_t page_size, int64_t n_free,
+                     int64_t n_rows, hipStream_t stream) {
+    if (!block_table || !seq_lens || !pages_used || !cached_lens || !new_lens) return QMM_ERR_NULL;
+    if ((n_rows > 0 && (!slots || !positions)) || (n_free > 0 && !free_pages)) return QMM_ERR_NULL;
+    if (batch < 1 || max_pages < 1 || n_free < 0 || n_rows < 0 || table_stride < max_pages) return QMM_ERR_SHAPE;
+    if (page_size < 1 || (page_size & (page_size - 1)) != 0) return QMM_ERR_SHAPE;
+    for (const void* p : {(const void*)block_table, (const void*)seq_lens, (const void*)slots, (const void*)positions,
+                          (const void*)pages_used, (const void*)cached_lens, (const void*)new_lens,
+                          (const void*)free_pages})
+        if (!aligned(p, 4)) return QMM_ERR_ALIGN;
+    int64_t cap, entries, span;
+    if (!mul_ok(max_pages, page_size, &cap) || !mul_ok(batch, max_pages, &entries) ||
+        !mul_ok(batch, table_stride, &span) || span > INT64_MAX / 4)
+        return QMM_ERR_SHAPE;
+    // lengths, page counts and rows are int32; a kernel stride past the last row or page stays one too
+    if (cap > KV_TOKENS_MAX || entries > KV_TOKENS_MAX || n_free > KV_TOKENS_MAX || n_rows > KV_TOKENS_MAX ||
+        batch > KV_TOKENS_MAX)
+        return QMM_ERR_RANGE;
+    const Span outs[] = {{block_table, ((batch - 1) * table_stride + max_pages) * 4}, {seq_lens, batch * 4},
+                         {slots, n_rows * 4}, {positions, n_rows * 4}, {pages_used, 4}};
+    for (int i = 0; i < 5; ++i) {
+        if (overlaps_any(outs[i].p, outs[i].n, {{cached_lens, batch * 4}, {new_lens, batch * 4}, {free_pages, n_free * 4}}))
+            return QMM_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QMM_ERR_ALIAS;
+    }
+    qmm::ExtendArgs a{block_table, table_stride, seq_lens, slots, positions, pages_used, cached_lens, new_lens,
+                      free_pages, (int)batch, log2_of(page_size), (int)n_free, (int)n_rows, cap};
+    qmm::launch_paged_extend(a, stream);
+    return launch_status();
+}
+
+int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const float* v, int64_t ldv,
+                  const int32_t* slots, int64_t n, hipStream_t stream) {
+    KvExtent e;
+    const int st = check_cache(cache, &e);
+    if (st) return st;
+    if (!k || !v || !slots) return QMM_ERR_NULL;
+    const int64_t row = cache->n_kv * cache->head_dim;
+    if (n < 1 || ldk < row || ldv < row) return QMM_ERR_SHAPE;
+    if (!aligned(k, 16) || !aligned(v, 16) || ldk % 4 != 0 || ldv % 4 != 0 || !aligned(slots, 4)) return QMM_ERR_ALIGN;
+    int64_t t1, t2, t3;
+    if (!mul_ok(n, ldk, &t1) || !mul_ok(n, ldv, &t2) || !mul_ok(n, cache->n_kv, &t3) || t1 > INT64_MAX / 4 ||
+        t2 > INT64_MAX / 4)
+        return QMM_ERR_SHAPE;
+    const Span ins[] = {{k, ((n - 1) * ldk + row) * 4}, {v, ((n - 1) * ldv + row) * 4}, {slots, n * 4}};
+    for (const Span& s : ins)
+        if (overlaps_any(s.p, s.n, {{cache->k, e.bytes}, {cache->v, e.bytes}, {cache->k_scale, e.scale_bytes},
+                                    {cache->v_scale, e.scale_bytes}}))
+            return QMM_ERR_ALIAS;
+    qmm::AppendArgs a{cache->k, cache->v, cache->k_scale, cache->v_scale, k, v, ldk, ldv, slots, n, (int)cache->n_kv,
+                      (int)(cache->n_pages * cache->page_size), log2_of(cache->page_size), cache->page_stride,
+                      cache->head_stride, cache->slot_stride, cache->scale_page_stride, cache->scale_head_stride,
+                      cache->scale_slot_stride};
+    qmm::launch_kv_append(a, cache->kind, (int)cache->head_dim, stream);
+    return launch_status();
+}
+
+int64_t qmm_paged_attention_workspace_bytes(int64_t batch, int64_t n_q, int64_t n_kv, int64_t head_dim,
+                                            int64_t max_pages, int64_t page_size) {
+    int64_t cap;
+    const int st = check_attention(batch, n_q, n_kv, head_dim, max_pages, page_size, &cap);
+    if (st) return -st;
+    return qmm::plan_paged_attention(batch, n_q, n_kv, head_dim, cap, dev_props().cu).ws_bytes;
+}
+
+int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int64_t ldq, const qmm_kv_cache* cache,
+                        const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens, int64_t batch,
+                        int64_t n_q, int64_t max_pages, float scale, void* workspace, int64_t workspace_bytes,
+                        hipStream_t stream) {
+    KvExtent e;
+    int st = check_cache(cache, &e);
+    if (st) return st;
+    if (!out || !q || !block_table || !seq_lens) return QMM_ERR_NULL;
+    int64_t cap;
+    st = check_attention(batch, n_q, cache->n_kv, cache->head_dim, max_pages, cache->page_size, &cap);
+    if (st) return st;
+    const int64_t row = n_q * cache->head_dim;
+    if (ldo < row || ldq < row || table_stride < max_pages) return QMM_ERR_SHAPE;
+    if (!aligned(out, 16) || !aligned(q, 16) || ldo % 4 != 0 || ldq % 4 != 0 || !aligned(lse, 4) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4))
+        return QMM_ERR_ALIGN;
+    int64_t t1, t2, t3;
+    if (!mul_ok(batch, ldo, &t1) || !mul_ok(batch, ldq, &t2) || !mul_ok(batch, table_stride, &t3) ||
+        t1 > INT64_MAX / 4 || t2 > INT64_MAX / 4 || t3 > INT64_MAX / 4)
+        return QMM_ERR_SHAPE;
+    if (!(scale - scale == 0.0f)) return QMM_ERR_RANGE;  // NaN or infinite
+    const qmm::AttnPlan pl = qmm::plan_paged_attention(batch, n_q, cache->n_kv, cache->head_dim, cap, dev_props().cu);
+    const Span sq{q, ((batch - 1) * ldq + row) * 4}, st_{block_table, ((batch - 1) * table_stride + max_pages) * 4},
+        sl{seq_lens, batch * 4}, sk{cache->k, e.bytes}, sv{cache->v, e.bytes}, sks{cache->k_scale, e.scale_bytes},
+        svs{cache->v_scale, e.scale_bytes};
+    const Span so{out, ((batch - 1) * ldo + row) * 4}, se{lse, lse ? batch * n_q * 4 : 0};
+    if (pl.ws_bytes > 0) {
+        if (!workspace) return QMM_ERR_NULL;
+        if (!aligned(workspace, 256)) return QMM_ERR_ALIGN;
+        if (workspace_bytes < pl.ws_bytes) return QMM_ERR_WORKSPACE;
+        if (overlaps_any(workspace, pl.ws_bytes, {sq, st_, sl, sk, sv, sks, svs, so, se})) return QMM_ERR_ALIAS;
+    }
+    if (overlaps_any(so.p, so.n, {sq, st_, sl, sk, sv, sks, svs, se}) ||
+        overlaps_any(se.p, se.n, {sq, st_, sl, sk, sv, sks, svs}))
+        return QMM_ERR_ALIAS;
+    const int64_t es = cache->kind == QMM_KV_Q8 ? 1 : 2;
+    qmm::AttnArgs a{};
+    a.out = out;
+    a.lse = lse;
+    a.q = q;
+    a.out_stride = ldo;
+    a.q_stride = ldq;
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.head_bytes = cache->head_stride * es;
+    a.page_units = (uint32_t)(cache->page_stride * es / 16);
+    a.slot_units = (uint32_t)(cache->slot_stride * es / 16);
+    a.scale_page = cache->scale_page_stride;
+    a.scale_head = cache->scale_head_stride;
+    a.scale_slot = cache->scale_slot_stride;
+    a.n_pages = (int)cache->n_pages;
+    a.page_log2 = log2_of(cache->page_size);
+    a.page_size = (int)cache->page_size;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.lens = seq_lens;
+    a.batch = (int)batch;
+    a.n_q = (int)n_q;
+    a.group = (int)(n_q / cache->n_kv);
+    a.capacity = (int)cap;
+    a.blocks_per_kv = pl.blocks_per_kv;
+    a.heads_per_block = pl.heads_per_block;
+    a.groups = pl.groups;
+    a.head_spaces = pl.head_spaces;
+    a.scale_log2e = scale * 1.4426950408889634f;
+    a.meta = pl.ws_bytes > 0 ? (int2*)workspace : nullptr;
+    a.parts = pl.ws_bytes > 0 ? (float*)((char*)workspace + pl.meta_bytes) : nullptr;
+    qmm::launch_paged_attention(a, cache->kind, (int)cache->head_dim, stream);
+    return launch_status();
+}
+
+int qmm_add_rmsnorm(float* y, int64_t ldy, float* h, int64_t ldh, const float* x, int64_t ldx, const float* residual,
+                    int64_t ldr, const float* weight, int64_t n, int64_t k, float eps, hipStream_t stream) {
+    if (!y) return QMM_ERR_NULL;
+    if (ldy < k) return QMM_ERR_SHAPE;
+    if (!aligned(y, 16) || ldy % 4 != 0) return QMM_ERR_ALIGN;
+    qmm::NormArgs a{};
+    a.y = y;
+    a.y_stride = ldy;
+    const int st = norm_args(&a, h, ldh, x, ldx, residual, ldr, weight, n, k, eps, 4, ldy);
+    if (st) return st;
+    qmm::launch_add_rmsnorm(a, stream);
+    return launch_status();
+}
+
+int qmm_add_rmsnorm_q8(int8_t* q, float* d, float* h, int64_t ldh, const float* x, int64_t ldx, const float* residual,
+                       int64_t ldr, const float* weight, int64_t n, int64_t k, float eps, hipStream_t stream) {
+    if (!q || !d) return QMM_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(d, 4)) return QMM_ERR_ALIGN;
+    qmm::NormArgs a{};
+    a.q = q;
+    a.d = d;
+    const int st = norm_args(&a, h, ldh, x, ldx, residual, ldr, weight, n, k, eps, 32, 0);
+    if (st) return st;
+    qmm::launch_add_rmsnorm(a, stream);
     return launch_status();
 }
 

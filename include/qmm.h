@@ -434,6 +434,167 @@ int qmm_nvfp4_repack_v2(void* dst, const void* src, int64_t rows, int64_t k, hip
 int qmm_stream_loadonly(uint32_t* sink, const void* w, int64_t m, int64_t k,
                         int qtype, hipStream_t stream);
 
+/*
+ * The operators of a decode step that stand between the projections: page
+ * tables, the paged key-value cache, attention over it, and the RMS norm.
+ * They follow the conventions at the top of this header.  Sizes that live in
+ * device memory (lengths, page ids, slots) cannot be checked on the host; a
+ * bad one never causes an out-of-range access, and each entry says what the
+ * call writes for it.
+ */
+
+/* Element kinds of a cache.  QMM_KV_Q8: int8 codes and one float scale per
+ * (token, head): an element is scale * code, -127 <= code <= 127. */
+typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8 = 2 } qmm_kv_kind;
+
+/*
+ * A paged key-value cache (a HOST struct; its pointers are DEVICE).  Element
+ * x of kv head h of the token in place s of page p is
+ *     k[p*page_stride + h*head_stride + s*slot_stride + x]
+ * and the same in v, so pages may hold heads outermost, tokens outermost, or
+ * both caches in one tensor.  A token's slot number is p*page_size + s.
+ *   k, v          16-byte aligned; strides in elements, each >= head_dim and
+ *                 a multiple of 16 bytes, giving every row bytes of its own.
+ *   k_scale, v_scale  QMM_KV_Q8 only (else ignored): float, strides in
+ *                 elements, each >= 1.
+ *   page_size     a power of two.  head_dim: a multiple of 32, at most 256
+ *                 (QMM_ERR_K_ALIGN, QMM_ERR_RANGE).
+ * Limits (QMM_ERR_RANGE): n_pages*page_size <= 2^30, n_kv <= 65535, 64 GiB
+ * from k's first to its last byte (and v's).  Unknown kind: QMM_ERR_QTYPE.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t n_pages, n_kv, page_size, head_dim;
+    int64_t page_stride, head_stride, slot_stride;
+    int64_t scale_page_stride, scale_head_stride, scale_slot_stride;
+    int32_t kind;
+} qmm_kv_cache;
+
+/*
+ * qmm_paged_extend: the page tables of a step, from the sequences' lengths.
+ * Sequence i holds c = cached_lens[i] tokens and gets n = new_lens[i] more.
+ * Pages it newly needs are taken from free_pages in sequence order: with
+ * have = ceil(c/P), need = ceil((c+n)/P) - have for pages of P = page_size
+ * tokens and first = the needs of the sequences before it,
+ *     block_table[i*table_stride + have + r] = free_pages[first + r], r < need
+ *     seq_lens[i] = c + n
+ * The new tokens' rows follow each other in sequence order (those of i start
+ * after the new_lens of the sequences before it); its r-th has
+ *     positions[row] = c + r
+ *     slots[row]     = block_table[..][(c+r)/P] * P + (c+r) % P
+ * Rows behind the last get slot and position -1 (qmm_kv_append skips such a
+ * row); rows from n_rows on are not written.  pages_used[0] = the pages the
+ * sequences need in all; the free list's next step starts behind them.
+ * Other table entries are left as they were, and no input is changed, so
+ * the call may be repeated.
+ * A sequence is refused where c or n is negative, c + n exceeds
+ * max_pages*page_size, or it needs pages and first + need > n_free (its pages
+ * count in pages_used, so pages_used > n_free tells of a shortage): its
+ * table row stays, seq_lens[i] = c, and its rows' slots are -1.  A row whose
+ * page is negative, or whose slot passes 2^31 - 1, gets slot -1.
+ *   block_table  DEVICE int32, batch rows of max_pages, table_stride >=
+ *                max_pages apart; read and written.
+ *   seq_lens [batch], slots [n_rows], positions [n_rows], pages_used [1]
+ *                DEVICE int32, written.
+ *   cached_lens, new_lens [batch], free_pages [n_free]  DEVICE int32.
+ *   n_rows, n_free >= 0 (their pointers may be null where 0); batch,
+ *   max_pages >= 1; max_pages*page_size, batch*max_pages, n_free and n_rows
+ *   at most 2^30 (QMM_ERR_RANGE).
+ */
+int qmm_paged_extend(int32_t* block_table, int64_t table_stride, int32_t* seq_lens, int32_t* slots,
+                     int32_t* positions, int32_t* pages_used, const int32_t* cached_lens, const int32_t* new_lens,
+                     const int32_t* free_pages, int64_t batch, int64_t max_pages, int64_t page_size, int64_t n_free,
+                     int64_t n_rows, hipStream_t stream);
+
+/*
+ * qmm_kv_append: new keys and values into their slots of the cache,
+ *     cache row (slots[t], h) = k[t*ldk + h*head_dim ..], v likewise,
+ * rounded to nearest even for QMM_KV_F16 and QMM_KV_BF16.  QMM_KV_Q8: per
+ * row, in f32, d = max|x| / 127 (0 where that is below the smallest normal),
+ * code = round-half-away-from-zero(x * (1/d)), or 0 when d = 0, as
+ * qmm_quantize_q8_1 does per block.  A row with a NaN or an infinity has no
+ * defined codes.
+ *   k, v    DEVICE float, n rows of n_kv*head_dim, ldk and ldv floats apart
+ *           (multiples of 4; rows of a fused projection's output), 16-byte
+ *           aligned.
+ *   slots   DEVICE int32[n].  A slot outside [0, n_pages*page_size) is
+ *           skipped.  The slots of one call must differ: a slot that is given
+ *           twice holds parts of either row.
+ */
+int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const float* v, int64_t ldv,
+                  const int32_t* slots, int64_t n, hipStream_t stream);
+
+/*
+ * qmm_paged_attention: attention of one new token per sequence over its
+ * cached tokens (the new one among them).  Query head h of n_q reads kv head
+ * h / (n_q/n_kv).  Over the tokens t < seq_lens[b], found through the
+ * sequence's row of block_table,
+ *     s_t = scale * sum_x q[b*ldq + h*head_dim + x] * k_t[x]
+ *     out[b*ldo + h*head_dim + x] = sum_t exp(s_t - M) v_t[x] / sum_t exp(s_t - M)
+ *     lse[b*n_q + h] = M + log(sum_t exp(s_t - M)),  M = max s_t
+ * A sequence of no tokens (a padded batch's row) gives zeros and lse = -inf.
+ * A length that is negative or above max_pages*page_size, and a page id
+ * outside [0, n_pages) among the pages that hold a sequence's tokens, give
+ * NaN for that sequence's outputs.  Table entries behind the last page, and
+ * cache rows behind the last token, are never used.  A non-finite query, key
+ * or value makes the outputs that it enters non-finite; the same holds for
+ * scores beyond the f32 range.
+ * f32 arithmetic: f32 operands enter the matrix cores as two f16 (three
+ * bf16) parts, products and sums are f32; the exponential and logarithm are
+ * the hardware's.
+ *   out   DEVICE float, rows ldo >= n_q*head_dim apart (a multiple of 4),
+ *         16-byte aligned.  lse: DEVICE float[batch*n_q] or NULL.
+ *   q     DEVICE float, rows ldq apart (as ldo), 16-byte aligned.
+ *   block_table  DEVICE int32, batch rows of max_pages, table_stride apart.
+ *   seq_lens     DEVICE int32[batch].
+ *   scale finite (QMM_ERR_RANGE).  n_q a multiple of n_kv.
+ *   workspace    DEVICE, 256-byte aligned, at least
+ *                qmm_paged_attention_workspace_bytes() bytes (may be NULL
+ *                where that is 0).  No initial contents are needed.  Calls
+ *                that share one must not overlap.
+ * Limits (QMM_ERR_RANGE): batch <= 2^20, n_q <= 65535, max_pages*page_size
+ * <= 2^30, batch*n_q and batch*ceil(max_pages*page_size/32) below 2^31.
+ */
+int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int64_t ldq, const qmm_kv_cache* cache,
+                        const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens, int64_t batch,
+                        int64_t n_q, int64_t max_pages, float scale, void* workspace, int64_t workspace_bytes,
+                        hipStream_t stream);
+
+/* Workspace bytes of qmm_paged_attention on the current device, a function
+ * of the sizes alone (never of the lengths); < 0 is -qmm_status. */
+int64_t qmm_paged_attention_workspace_bytes(int64_t batch, int64_t n_q, int64_t n_kv, int64_t head_dim,
+                                            int64_t max_pages, int64_t page_size);
+
+/*
+ * qmm_add_rmsnorm: residual addition and RMS norm,
+ *     h = x + residual (x where residual is NULL; f32)
+ *     y = h * weight / sqrt(mean over k of h^2 + eps)
+ *   y         DEVICE float, n rows ldy apart, written.
+ *   h         DEVICE float, n rows ldh apart, written; NULL: not kept.
+ *   x, residual  DEVICE float, n rows ldx (ldr) apart.  weight: float[k].
+ *   k         a multiple of 4 (QMM_ERR_K_ALIGN), at most 2^24; row strides
+ *             >= k and multiples of 4; every pointer 16-byte aligned.
+ *   eps       finite and >= 0 (QMM_ERR_RANGE).
+ */
+int qmm_add_rmsnorm(float* y, int64_t ldy, float* h, int64_t ldh, const float* x, int64_t ldx, const float* residual,
+                    int64_t ldr, const float* weight, int64_t n, int64_t k, float eps, hipStream_t stream);
+
+/*
+ * qmm_add_rmsnorm_q8: qmm_add_rmsnorm with y as Q8_1 activations (for the _q8
+ * MoE projections).  1/rms is one factor of a whole row, so codes are those
+ * of z = h * weight: per block of 32, in f32, d0 = max|z| / 127 (0 where that
+ * is below the smallest normal), q = round-half-away-from-zero(z * (1/d0)),
+ * or 0 when d0 = 0, and d = d0 / sqrt(mean h^2 + eps).
+ *   q     DEVICE int8[n*k], 16-byte aligned.  d: DEVICE float[n*k/32].
+ *   k     a multiple of 32.
+ * Other arguments as qmm_add_rmsnorm.
+ */
+int qmm_add_rmsnorm_q8(int8_t* q, float* d, float* h, int64_t ldh, const float* x, int64_t ldx, const float* residual,
+                       int64_t ldr, const float* weight, int64_t n, int64_t k, float eps, hipStream_t stream);
+
 /* Packed bytes of one row of k weights; < 0 is -qmm_status on error.
  * (Sizes per the VARIANTS table of cera wgpu_gemm_bench.rs and memra
  * synth_rows.) */
