@@ -579,13 +579,18 @@ class KVCache:
             scale_strides = _view_strides(k_scale, 3, "k_scale", 1)
             if scale_strides != _view_strides(v_scale, 3, "v_scale", 1):
                 raise ValueError("k_scale and v_scale must have the same strides")
-        self.device = _same_device(k, v, *(() if k_scale is None else (k_scale, v_scale)))
+        self.device = k.device
+        for t in (v,) if k_scale is None else (v, k_scale, v_scale):
+            if t.device != k.device:
+                raise ValueError(f"tensors on {k.device} and {t.device}")
+        self._index = k.get_device()
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv, self.page_size, self.head_dim = k.shape
         self._struct = _KvCacheStruct(
             k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
             None if v_scale is None else v_scale.data_ptr(), *k.shape, *strides, *scale_strides, KV_KINDS[self.kind])
         self._ptr = ctypes.addressof(self._struct)
+        self._row = self.n_kv * self.head_dim
 
 
 def _view_strides(t, n: int, what: str, least=None):
@@ -604,74 +609,67 @@ def _view_strides(t, n: int, what: str, least=None):
     return strides
 
 
-def _same_device(*tensors):
-    device = tensors[0].device
-    for t in tensors[1:]:
-        if t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    return device
-
-
-def _i32(t, what, shape=None):
-    """Pointer of a contiguous int32 device tensor (of a shape)."""
+# The calls below are a decode step's small kernels, a few microseconds each: their checks read
+# every tensor's type, device (get_device is -1 on the host), shape and strides once and leave the
+# wording of a refusal to _refuse.
+def _refuse(t, what, dtype, dev, shape):
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
-        raise TypeError(f"{what} must be an int32 device (cuda/hip) tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        got = f"{t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise TypeError(f"{what} must be a {dtype} device (cuda/hip) tensor, got {got}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, other tensors on device {dev}")
+    raise ValueError(f"{what} must be {shape}, got {list(t.shape)} with strides {list(t.stride())}")
 
 
-def _f32_rows(t, what, n, row, heads=0):
-    """(pointer, row stride) of a float32 device tensor [n, row], or [n, heads, row / heads] with
-    its heads side by side; rows any stride apart."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
-        raise TypeError(f"{what} must be a float32 device (cuda/hip) tensor")
-    shape, stride = t.shape, t.stride()
-    if heads and len(shape) == 3:
-        ok = shape == (n, heads, row // heads) and (heads == 1 or stride[1] == row // heads)
+def _packed(torch, t, what, dtype, dev, shape):
+    """Pointer of a contiguous tensor of this shape."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return _refuse(t, what, dtype, dev, f"contiguous {list(shape)}")
+
+
+def _f32_rows(torch, t, what, dev, n, row, heads=0):
+    """(pointer, row stride) of a float32 tensor [n, row], or [n, heads, row / heads] with its heads
+    side by side; rows any stride apart."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == dev:
+        shape = t.shape
+        if shape == (n, row) or (heads and shape == (n, heads, row // heads)):
+            if t.is_contiguous():
+                return t.data_ptr(), row
+            stride = t.stride()
+            if stride[-1] == 1 and (len(shape) == 2 or heads == 1 or stride[1] == row // heads):
+                return t.data_ptr(), (stride[0] if n > 1 else row)
+    return _refuse(t, what, torch.float32, dev,
+                   f"[{n}, {row}]" + (f" or [{n}, {heads}, {row // heads}]" if heads else "") + " with contiguous rows")
+
+
+def _table(torch, t, dev, batch):
+    """(pointer, entries per row, row stride) of a block table."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and t.dim() == 2:
+        n, width = t.shape
+        ld, unit = t.stride()
+        if n == batch and (unit == 1 or width == 1):
+            return t.data_ptr(), width, (ld if n > 1 else width)
+    return _refuse(t, "block_table", torch.int32, dev, f"[{batch}, max_pages] with contiguous rows")
+
+
+def _call(torch, dev, name, *args, stream):
+    """A library call on device dev, on the given stream or the device's current one."""
+    f = getattr(_LIB, name)
+    if torch._C._cuda_getDevice() == dev:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     else:
-        ok = shape == (n, row)
-    if not ok or (shape[-1] > 1 and stride[-1] != 1):
-        want = f"[{n}, {row}]" + (f" or [{n}, {heads}, {row // heads}]" if heads else "")
-        raise ValueError(f"{what} must be {want} with contiguous rows, got {list(shape)} with strides {list(stride)}")
-    return t.data_ptr(), (stride[0] if n > 1 else (row + 3) // 4 * 4)
+        with torch.cuda.device(dev):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise QmmError(st, name)
 
 
-def _table(t, batch, what="block_table"):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
-        raise TypeError(f"{what} must be an int32 device (cuda/hip) tensor")
-    if t.dim() != 2 or t.shape[0] != batch or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be [{batch}, max_pages] with unit stride along its rows")
-    return t.data_ptr(), t.shape[1], (t.stride(0) if batch > 1 else t.shape[1])
-
-
-class _On:
-    """Makes a tensor's device the current one, where it is not."""
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        import torch
-        self.guard = None
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _stream_on(device, stream):
-    """Handle of the given stream, or of the device's current one."""
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+def _device_of(torch, t, what):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a device (cuda/hip) tensor")
+    return t.get_device()
 
 
 def paged_extend(block_table, cached_lens, new_lens, free_pages, page_size: int, n_rows: int, seq_lens=None,
@@ -683,25 +681,27 @@ def paged_extend(block_table, cached_lens, new_lens, free_pages, page_size: int,
     after sequence, -1 behind the last row and (slots) for a sequence that is refused because its
     table row or the free list is too short: its seq_lens entry stays cached_lens."""
     import torch
-    lib = load()
+    load()
+    dev = _device_of(torch, block_table, "block_table")
+    i32 = torch.int32
     batch = cached_lens.shape[0]
-    table, max_pages, table_stride = _table(block_table, batch)
-    device = block_table.device
-    new = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
-    seq_lens = new(batch) if seq_lens is None else seq_lens
-    slots = new(n_rows) if slots is None else slots
-    positions = new(n_rows) if positions is None else positions
-    pages_used = new(1) if pages_used is None else pages_used
-    _same_device(block_table, cached_lens, new_lens, free_pages, seq_lens, slots, positions, pages_used)
-    with _On(device):
-        st = lib.qmm_paged_extend(
-            table, table_stride, _i32(seq_lens, "seq_lens", (batch,)), _i32(slots, "slots", (n_rows,)),
-            _i32(positions, "positions", (n_rows,)), _i32(pages_used, "pages_used", (1,)),
-            _i32(cached_lens, "cached_lens", (batch,)), _i32(new_lens, "new_lens", (batch,)),
-            _i32(free_pages, "free_pages", (free_pages.numel(),)), batch, max_pages, page_size, free_pages.numel(),
-            n_rows, _stream_on(device, stream))
-    if st != 0:
-        raise QmmError(st, "qmm_paged_extend")
+    n_free = free_pages.numel()
+    table, max_pages, ld = _table(torch, block_table, dev, batch)
+    if seq_lens is None:
+        seq_lens = torch.empty(batch, dtype=i32, device=block_table.device)
+    if slots is None:
+        slots = torch.empty(n_rows, dtype=i32, device=block_table.device)
+    if positions is None:
+        positions = torch.empty(n_rows, dtype=i32, device=block_table.device)
+    if pages_used is None:
+        pages_used = torch.empty(1, dtype=i32, device=block_table.device)
+    one, rows = (batch,), (n_rows,)
+    _call(torch, dev, "qmm_paged_extend", table, ld, _packed(torch, seq_lens, "seq_lens", i32, dev, one),
+          _packed(torch, slots, "slots", i32, dev, rows), _packed(torch, positions, "positions", i32, dev, rows),
+          _packed(torch, pages_used, "pages_used", i32, dev, (1,)),
+          _packed(torch, cached_lens, "cached_lens", i32, dev, one), _packed(torch, new_lens, "new_lens", i32, dev, one),
+          _packed(torch, free_pages, "free_pages", i32, dev, (n_free,)), batch, max_pages, page_size, n_free, n_rows,
+          stream=stream)
     return seq_lens, slots, positions, pages_used
 
 
@@ -709,21 +709,19 @@ def kv_append(cache: KVCache, k, v, slots, stream=None):
     """Writes new keys and values (float32 [n, n_kv, head_dim], or [n, n_kv*head_dim]; rows any
     stride apart, as views of a fused projection's output) into their slots (int32 [n]; a slot
     outside the cache, such as -1, is skipped; the others must differ)."""
-    lib = load()
+    import torch
+    load()
+    dev, row, heads = cache._index, cache._row, cache.n_kv
     n = slots.shape[0]
-    row = cache.n_kv * cache.head_dim
-    _same_device(cache.k, k, v, slots)
-    with _On(cache.device):
-        st = lib.qmm_kv_append(cache._ptr, *_f32_rows(k, "k", n, row, cache.n_kv),
-                               *_f32_rows(v, "v", n, row, cache.n_kv), _i32(slots, "slots", (n,)), n,
-                               _stream_on(cache.device, stream))
-    if st != 0:
-        raise QmmError(st, "qmm_kv_append")
+    _call(torch, dev, "qmm_kv_append", cache._ptr, *_f32_rows(torch, k, "k", dev, n, row, heads),
+          *_f32_rows(torch, v, "v", dev, n, row, heads), _packed(torch, slots, "slots", torch.int32, dev, (n,)), n,
+          stream=stream)
 
 
 def paged_attention_workspace_bytes(batch: int, n_q: int, cache: KVCache, max_pages: int) -> int:
     """Bytes of workspace paged_attention uses for these sizes (0: none)."""
-    with _On(cache.device):
+    import torch
+    with torch.cuda.device(cache.device):
         r = load().qmm_paged_attention_workspace_bytes(batch, n_q, cache.n_kv, cache.head_dim, max_pages, cache.page_size)
     if r < 0:
         raise QmmError(-r, "qmm_paged_attention_workspace_bytes")
@@ -741,58 +739,41 @@ def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=No
     paged_attention_workspace_bytes() bytes that no other call uses at the same time."""
     import torch
     lib = load()
+    dev, d = cache._index, cache.head_dim
     batch = seq_lens.shape[0]
-    d = cache.head_dim
     n_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
-    qp, ldq = _f32_rows(q, "q", batch, n_q * d, n_q)
+    row = n_q * d
+    qp, ldq = _f32_rows(torch, q, "q", dev, batch, row, n_q)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    op, ldo = _f32_rows(out, "out", batch, n_q * d, n_q)
-    table, max_pages, table_stride = _table(block_table, batch)
-    lp = None
-    if lse is not None:
-        lp = _dev(lse, "lse", torch.float32)
-        if lse.shape != (batch, n_q):
-            raise ValueError(f"lse must be [{batch}, {n_q}]")
-        _same_device(q, lse)
-    _same_device(cache.k, q, out, block_table, seq_lens)
-    device = cache.device
-    with _On(device):
-        nbytes = lib.qmm_paged_attention_workspace_bytes(batch, n_q, cache.n_kv, d, max_pages, cache.page_size)
-        ws, ws_len = None, 0
-        if nbytes > 0:
-            if isinstance(workspace, str):
-                if workspace != "auto":
-                    raise ValueError("workspace must be 'auto' or a tensor")
+    op, ldo = _f32_rows(torch, out, "out", dev, batch, row, n_q)
+    table, max_pages, ld = _table(torch, block_table, dev, batch)
+    lp = None if lse is None else _packed(torch, lse, "lse", torch.float32, dev, (batch, n_q))
+    lens = _packed(torch, seq_lens, "seq_lens", torch.int32, dev, (batch,))
+    ws, ws_len = None, 0
+    if workspace is not None:
+        if isinstance(workspace, str):
+            if workspace != "auto":
+                raise ValueError("workspace must be 'auto', None or a tensor")
+            if torch._C._cuda_getDevice() == dev:
+                ws_len = lib.qmm_paged_attention_workspace_bytes(batch, n_q, cache.n_kv, d, max_pages, cache.page_size)
+            else:
+                ws_len = paged_attention_workspace_bytes(batch, n_q, cache, max_pages)
+            if ws_len > 0:
                 if stream is None:
-                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                    workspace = torch.empty(ws_len, dtype=torch.uint8, device=cache.device)
                 else:
-                    # memory of the stream that uses it
-                    with torch.cuda.stream(stream):
-                        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            if workspace is not None:
-                _same_device(q, workspace)
-                ws, ws_len = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-        st = lib.qmm_paged_attention(op, ldo, lp, qp, ldq, cache._ptr, table, table_stride,
-                                     _i32(seq_lens, "seq_lens", (batch,)), batch, n_q, max_pages,
-                                     d ** -0.5 if scale is None else scale, ws, ws_len, _stream_on(device, stream))
-    if st != 0:
-        raise QmmError(st, "qmm_paged_attention")
+                    with torch.cuda.stream(stream):     # memory of the stream that uses it
+                        workspace = torch.empty(ws_len, dtype=torch.uint8, device=cache.device)
+                ws = workspace.data_ptr()
+            else:
+                ws_len = 0
+        else:
+            ws_len = workspace.numel() * workspace.element_size()
+            ws = _packed(torch, workspace, "workspace", workspace.dtype, dev, workspace.shape)
+    _call(torch, dev, "qmm_paged_attention", op, ldo, lp, qp, ldq, cache._ptr, table, ld, lens, batch, n_q, max_pages,
+          d ** -0.5 if scale is None else scale, ws, ws_len, stream=stream)
     return out
-
-
-def _norm_rows(x, weight, residual, h):
-    """The arguments that both norms share: h's, x's and residual's pointers and strides, weight's
-    pointer, n, k."""
-    import torch
-    n, k = x.shape
-    xp, ldx = _f32_rows(x, "x", n, k)
-    rp, ldr = (None, 0) if residual is None else _f32_rows(residual, "residual", n, k)
-    hp, ldh = (None, 0) if h is None else _f32_rows(h, "h", n, k)
-    if weight.shape != (k,):
-        raise ValueError(f"weight must be [{k}]")
-    _same_device(x, weight, *(t for t in (residual, h) if t is not None))
-    return hp, ldh, xp, ldx, rp, ldr, _dev(weight, "weight", torch.float32), n, k
 
 
 def add_rmsnorm(x, weight, residual=None, eps: float = 1e-5, y=None, h=None, stream=None):
@@ -800,18 +781,17 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-5, y=None, h=None, str
     unless a tensor is given for it) and y = h * weight / sqrt(mean(h*h) + eps), float32 [n, k],
     k a multiple of 4.  Rows of any of them may be any multiple of 4 apart."""
     import torch
-    lib = load()
+    load()
+    dev = _device_of(torch, x, "x")
+    n, k = x.shape
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+        y = torch.empty((n, k), dtype=torch.float32, device=x.device)
     if h is None and residual is not None:
-        h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
-    args = _norm_rows(x, weight, residual, h)
-    yp, ldy = _f32_rows(y, "y", *x.shape)
-    device = _same_device(x, y)
-    with _On(device):
-        st = lib.qmm_add_rmsnorm(yp, ldy, *args, eps, _stream_on(device, stream))
-    if st != 0:
-        raise QmmError(st, "qmm_add_rmsnorm")
+        h = torch.empty((n, k), dtype=torch.float32, device=x.device)
+    _call(torch, dev, "qmm_add_rmsnorm", *_f32_rows(torch, y, "y", dev, n, k),
+          *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)), *_f32_rows(torch, x, "x", dev, n, k),
+          *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
+          _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps, stream=stream)
     return y, h
 
 
@@ -819,21 +799,18 @@ def add_rmsnorm_q8(x, weight, residual=None, eps: float = 1e-5, q=None, d=None, 
     """add_rmsnorm with y as Q8_1 activations; returns (q int8 [n, k], d float32 [n, k/32], h), q
     and d as moe_gateup_q8 takes them.  k a multiple of 32."""
     import torch
-    lib = load()
+    load()
+    dev = _device_of(torch, x, "x")
     n, k = x.shape
     if q is None:
         q = torch.empty((n, k), dtype=torch.int8, device=x.device)
     if d is None:
         d = torch.empty((n, k // 32), dtype=torch.float32, device=x.device)
     if h is None and residual is not None:
-        h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
-    if q.shape != (n, k) or d.shape != (n, k // 32):
-        raise ValueError(f"q must be [{n}, {k}] and d [{n}, {k // 32}]")
-    args = _norm_rows(x, weight, residual, h)
-    device = _same_device(x, q, d)
-    with _On(device):
-        st = lib.qmm_add_rmsnorm_q8(_dev(q, "q", torch.int8), _dev(d, "d", torch.float32), *args, eps,
-                                    _stream_on(device, stream))
-    if st != 0:
-        raise QmmError(st, "qmm_add_rmsnorm_q8")
+        h = torch.empty((n, k), dtype=torch.float32, device=x.device)
+    _call(torch, dev, "qmm_add_rmsnorm_q8", _packed(torch, q, "q", torch.int8, dev, (n, k)),
+          _packed(torch, d, "d", torch.float32, dev, (n, k // 32)),
+          *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)), *_f32_rows(torch, x, "x", dev, n, k),
+          *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
+          _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps, stream=stream)
     return q, d, h
