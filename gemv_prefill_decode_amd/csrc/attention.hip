@@ -32,7 +32,7 @@
 // lengths are: every work group scans the lengths itself, so no host plan or
 // length is needed.  A unit inside one wave is finished there; parts of a unit
 // are joined in LDS, or, where it spans work groups, by a second kernel from
-// the workspace, always in token order, so results do not vary between calls.
+// the workspace, always in the same order, so results do not vary between calls.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -426,106 +426,130 @@ __host__ __device__ __forceinline__ int part_floats(int heads_per_block, int d) 
 // number is at least 1/x below it, so rounding to 53 bits does not reach it.
 __device__ __forceinline__ int64_t floor_div(int64_t x, int64_t y) { return (int64_t)((double)x / (double)y); }
 
+// Sum over the wave's lanes up to this one: row shifts within 16 lanes, then
+// the rows' last lanes handed on (no LDS).
+__device__ __forceinline__ int wave_inclusive(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
+// A wave's run of tiles [pos, end) of the axis of all units' tiles, and where
+// it begins: unit (head space, sequence), tile in it.
+struct Run {
+    int64_t pos, end;
+    int hs, b, t;
+};
+
+// Cuts the axis into a.groups equal chunks, a quarter per wave; *run: wave w's
+// of chunk g (*lo: the chunk's first tile).  Every wave scans the lengths by
+// itself, its lanes a run of consecutive sequences each.  Returns the tiles of
+// a chunk.
+__device__ __forceinline__ int64_t cut(const AttnArgs& a, int g, int w, int64_t* lo, Run* run) {
+    const int lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
+    const int b_lo = lane * per, b_hi = b_lo + per < a.batch ? b_lo + per : a.batch;
+    int mine = 0;
+#pragma unroll 8
+    for (int b = b_lo; b < b_hi; ++b) mine += seq_tiles(seq_len(a, b));
+    const int incl = wave_inclusive(mine), before = incl - mine;
+    const int total = __builtin_amdgcn_readlane(incl, 63);  // tiles per head space
+    const int64_t all = (int64_t)total * a.head_spaces;
+    int64_t chunk = (int64_t)((double)(all + a.groups - 1) * a.inv_groups);
+    if (chunk * a.groups < all) ++chunk;  // the product rounded across a whole number
+    chunk = (chunk + 3) & ~(int64_t)3;    // at least a tile per wave
+    *lo = g * chunk;
+    const int64_t hi = *lo + chunk < all ? *lo + chunk : all;
+    run->pos = *lo + w * (chunk >> 2);
+    run->end = run->pos + (chunk >> 2) < hi ? run->pos + (chunk >> 2) : hi;
+    if (run->pos >= run->end) return chunk;
+    run->hs = (int)floor_div(run->pos, total);
+    const int r = (int)(run->pos - (int64_t)run->hs * total);
+    const int src = __builtin_ctzll(__ballot(r >= before && r < incl));
+    int at = __builtin_amdgcn_readlane(before, src), b = src * per;
+    if (per > 1)
+        for (;; ++b) {
+            const int nt = seq_tiles(seq_len(a, b));
+            if (r < at + nt) break;
+            at += nt;
+        }
+    run->b = b;
+    run->t = r - at;
+    return chunk;
+}
+
 template <int KIND, int NB>
 __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void paged_attn_kernel(const AttnArgs a) {
     constexpr int D = 32 * NB;
     extern __shared__ __attribute__((aligned(16))) float parts[];  // [wave][2] parts
-    __shared__ int wsum[4];
-    __shared__ int start_hs[4], start_b[4], start_t[4];
-    __shared__ int part_unit[4][2], part_ends[4][2], part_follow[4];
+    __shared__ int part_unit[4][2], part_ends[4][2];
+    __shared__ int2 out_unit;  // the unit that starts here and goes on in the next work groups, and in how many
     const int tid = threadIdx.x, w = uni(tid >> 6), lane = tid & 63;
     const int g = blockIdx.x;
 
-    // tiles per head space: each thread counts a run of consecutive sequences
-    const int per = (a.batch + 255) / 256;
-    const int b_lo = tid * per, b_hi = b_lo + per < a.batch ? b_lo + per : a.batch;
-    int mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += seq_tiles(seq_len(a, b));
-    int incl = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const int v = __shfl_up(incl, s);
-        if (lane >= s) incl += v;
+    int64_t chunk = 0;
+    Run run;
+    if (a.per_unit) {
+        const int nt = seq_tiles(seq_len(a, g)), quarter = (nt + 3) / 4;
+        run.hs = blockIdx.y;
+        run.b = g;
+        run.pos = run.t = w * quarter;
+        run.end = run.pos + quarter < nt ? run.pos + quarter : nt;
+    } else {
+        int64_t lo;
+        chunk = cut(a, g, w, &lo, &run);
     }
-    if (lane == 63) wsum[w] = incl;
-    if (tid < 8) part_unit[tid >> 1][tid & 1] = -1;
-    __syncthreads();
-    int before = incl - mine, total = 0;
-    for (int i = 0; i < 4; ++i) {
-        if (i < w) before += wsum[i];
-        total += wsum[i];
-    }
-    total = uni(total);
-    const int64_t all = (int64_t)total * a.head_spaces;
-    int64_t chunk = floor_div(all + a.groups - 1, a.groups);
-    chunk = (chunk + 3) & ~(int64_t)3;  // at least a tile per wave
-    const int64_t lo = g * chunk, hi = lo + chunk < all ? lo + chunk : all;
-    if (lo >= all) {
-        if (tid == 0 && a.meta) a.meta[g] = make_int2(0, 0);
-        return;
-    }
-    const int64_t wc = chunk >> 2;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t x = lo + i * wc;
-        if (x >= hi) break;
-        const int hs = (int)floor_div(x, total), r = (int)(x - (int64_t)hs * total);
-        if (r >= before && r < before + mine) {
-            int at = before, b = b_lo;
-            for (;; ++b) {
-                const int nt = seq_tiles(seq_len(a, b));
-                if (r < at + nt) break;
-                at += nt;
-            }
-            start_hs[i] = hs;
-            start_b[i] = b;
-            start_t[i] = r - at;
-        }
-    }
-    __syncthreads();
+    if (lane < 2) part_unit[w][lane] = -1;
+    if (tid == 0) out_unit = make_int2(0, 0);
+    if (!a.per_unit && !a.meta_by_unit) __syncthreads();
 
     const int pf = part_floats(a.heads_per_block, D);
-    int64_t pos = lo + w * wc;
-    const int64_t end = pos + wc < hi ? pos + wc : hi;
-    if (pos < end) {
-        int hs = uni(start_hs[w]), b = uni(start_b[w]), t = uni(start_t[w]);
-        while (pos < end) {
-            const int len = uni(seq_len(a, b)), nt = seq_tiles(len);
-            const int n = (int)(nt - t < end - pos ? nt - t : end - pos);
-            const Unit u = unit_of(a, hs, b);
-            Segment<KIND, NB> seg;
-            seg.run(a, b, len, u.kvh, u.head0, u.rows, t, n);
-            const int i = lane & 15;
-            if (n == nt) {  // the whole unit: its outputs
-                if (i < u.rows) {
-                    const float inv = len == 0 ? 0.0f : 1.0f / seg.l;
-                    float* o = a.out + (int64_t)b * a.out_stride + (int64_t)(u.head0 + i) * D;
-                    seg.each(inv, [&](int d, auto v) { *(decltype(v)*)(o + d) = v; });
-                    if (a.lse && lane < 16)
-                        a.lse[(int64_t)b * a.n_q + u.head0 + i] = len == 0 ? -INFINITY : lse_of(seg.m, seg.l);
-                }
-            } else {
-                const int slot = t == 0 ? 1 : 0;
-                float* o = parts + (w * 2 + slot) * pf;
-                if (i < a.heads_per_block) {
-                    float* row = o + i * D;
-                    seg.each(1.0f, [&](int d, auto v) { *(decltype(v)*)(row + d) = v; });
-                    if (lane < 16) {
-                        o[a.heads_per_block * D + 2 * i] = seg.m;
-                        o[a.heads_per_block * D + 2 * i + 1] = seg.l;
-                    }
-                }
-                if (lane == 0) {
-                    part_unit[w][slot] = hs * a.batch + b;
-                    part_ends[w][slot] = t + n == nt;
-                    if (slot) part_follow[w] = (int)floor_div(pos + nt - 1, chunk) - g;
-                }
+    while (run.pos < run.end) {
+        const int b = uni(run.b), t = uni(run.t), hs = uni(run.hs);
+        const int len = uni(seq_len(a, b)), nt = seq_tiles(len);
+        const int n = (int)(nt - t < run.end - run.pos ? nt - t : run.end - run.pos);
+        const Unit u = unit_of(a, hs, b);
+        Segment<KIND, NB> seg;
+        seg.run(a, b, len, u.kvh, u.head0, u.rows, t, n);
+        const int i = lane & 15;
+        if (n == nt) {  // the whole unit: its outputs
+            if (i < u.rows) {
+                const float inv = len == 0 ? 0.0f : 1.0f / seg.l;
+                float* o = a.out + (int64_t)b * a.out_stride + (int64_t)(u.head0 + i) * D;
+                seg.each(inv, [&](int d, auto v) { *(decltype(v)*)(o + d) = v; });
+                if (a.lse && lane < 16)
+                    a.lse[(int64_t)b * a.n_q + u.head0 + i] = len == 0 ? -INFINITY : lse_of(seg.m, seg.l);
             }
-            pos += n;
-            t = 0;
-            if (++b == a.batch) {
-                b = 0;
-                ++hs;
+        } else {
+            const int slot = t == 0 ? 1 : 0;  // the unit starts in this wave, or came in from the one before
+            float* o = parts + (w * 2 + slot) * pf;
+            if (i < a.heads_per_block) {
+                float* row = o + i * D;
+                seg.each(1.0f, [&](int d, auto v) { *(decltype(v)*)(row + d) = v; });
+                if (lane < 16) *(f32x2*)(o + a.heads_per_block * D + 2 * i) = f32x2{seg.m, seg.l};
             }
+            if (lane == 0) {
+                part_unit[w][slot] = hs * a.batch + b;
+                part_ends[w][slot] = t + n == nt;
+            }
+        }
+        if (t == 0 && !a.per_unit) {  // work groups after this one that share the unit
+            const int follow = n == nt ? 0 : (int)floor_div(run.pos + nt - 1, chunk) - g;
+            if (a.meta_by_unit) {
+                if (lane == 0) a.meta[hs * a.batch + b] = make_int2(g, follow);
+            } else if (follow && lane == 0) {
+                out_unit = make_int2(hs * a.batch + b, follow);
+            }
+        }
+        run.pos += n;
+        run.t = 0;
+        run.b = b + 1;
+        if (run.b == a.batch) {
+            run.b = 0;
+            run.hs = hs + 1;
         }
     }
     __syncthreads();
@@ -533,7 +557,6 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void paged_attn_kernel(const 
     // Join the parts of each unit, in token order: a unit that starts here
     // (slot 1 of some wave) or came in from the previous work group (slot 0 of
     // wave 0), and the slots 0 of the following waves up to its end.
-    int2 info = make_int2(0, 0);
     for (int first = -1; first < 4; ++first) {
         const int w0 = first < 0 ? 0 : first, s0 = first < 0 ? 0 : 1;
         const int unit = part_unit[w0][s0];
@@ -544,7 +567,6 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void paged_attn_kernel(const 
         const Unit u = unit_of(a, unit / a.batch, unit % a.batch);
         const bool whole = s0 == 1 && ends;
         float* ws = whole ? nullptr : a.parts + (int64_t)(2 * g + s0) * pf;
-        if (s0 == 1 && !ends) info = make_int2(unit + 1, part_follow[w0]);
         for (int x = tid; x < u.rows * (D / 4); x += 256) {
             const int row = x / (D / 4), d = 4 * (x % (D / 4));
             const float* ml = parts + a.heads_per_block * D + 2 * row;
@@ -554,78 +576,124 @@ __global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void paged_attn_kernel(const 
             f32x4 o = {0, 0, 0, 0};
             float l = 0.0f;
             for (int v = w0; v <= last; ++v) {
-                const int at = (v * 2 + (v == w0 ? s0 : 0)) * pf;
-                const float f = __builtin_amdgcn_exp2f(ml[at] - base);
-                o += *(const f32x4*)(parts + at + row * D + d) * f;
-                l += ml[at + 1] * f;
+                const int p = (v * 2 + (v == w0 ? s0 : 0)) * pf;
+                const float f = __builtin_amdgcn_exp2f(ml[p] - base);
+                o += *(const f32x4*)(parts + p + row * D + d) * f;
+                l += ml[p + 1] * f;
             }
             if (whole) {
                 *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * D + d) = o * (1.0f / l);
                 if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l);
             } else {
                 *(f32x4*)(ws + row * D + d) = o;
-                if (d == 0) {
-                    ws[a.heads_per_block * D + 2 * row] = top;
-                    ws[a.heads_per_block * D + 2 * row + 1] = l;
-                }
+                if (d == 0) *(f32x2*)(ws + a.heads_per_block * D + 2 * row) = f32x2{top, l};
             }
         }
     }
-    if (tid == 0 && a.meta) a.meta[g] = info;
+    if (tid == 0 && !a.per_unit && !a.meta_by_unit) a.meta[g] = out_unit;
 }
 
-// The units that span work groups.  A work group's last unit may continue in
-// the following ones (meta: its number + 1, and how many); its parts are part
-// 1 of that work group and part 0 of the others.  One work group of this
-// kernel per such unit and query head: threads take (part, four dimensions),
-// parts a thread group apart, then the thread groups' sums are added in order.
+// The units that span work groups.  Its parts are part 1 of the work group it
+// starts in and part 0 of the following ones; meta says where and how many.
+// An entry per unit, or per work group where the units are more (a work group
+// starts at most one such unit): {work group or unit, following work groups}.
+struct Split {
+    Unit u;
+    int g, n;  // first work group, parts
+};
+__device__ __forceinline__ Split split_of(const AttnArgs& a) {
+    const int2 info = a.meta[blockIdx.x];
+    const int unit = a.meta_by_unit ? blockIdx.x : info.x;
+    Split s;
+    s.g = a.meta_by_unit ? info.x : blockIdx.x;
+    s.n = info.y == 0 ? 0 : info.y + 1;
+    if (s.n) s.u = unit_of(a, unit / a.batch, unit % a.batch);
+    return s;
+}
+
+struct Sum {
+    f32x4 o = {0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;
+    __device__ __forceinline__ void add(f32x4 v, float m2, float l2) {
+        const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.0f : top;
+        const float f = __builtin_amdgcn_exp2f(m - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
+        o = o * f + v * f2;
+        l = l * f + l2 * f2;
+        m = top;
+    }
+    // parts p0, p0 + step, .. of a split unit, eight in flight
+    __device__ __forceinline__ void parts(const AttnArgs& a, const Split& s, int dim, int row, int d, int p0, int step) {
+        const int pf = part_floats(a.heads_per_block, dim), ml0 = a.heads_per_block * dim + 2 * row;
+        for (; p0 < s.n; p0 += 8 * step) {
+            f32x4 v[8];
+            f32x2 ml[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int p = p0 + j * step < s.n ? p0 + j * step : p0;
+                const float* at = a.parts + (int64_t)(2 * (s.g + p) + (p == 0 ? 1 : 0)) * pf;
+                v[j] = *(const f32x4*)(at + row * dim + d);
+                ml[j] = *(const f32x2*)(at + ml0);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (p0 + j * step < s.n) add(v[j], ml[j].x, ml[j].y);
+        }
+    }
+    __device__ __forceinline__ void write(const AttnArgs& a, const Unit& u, int dim, int row, int d) const {
+        *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * dim + d) = o * (1.0f / l);
+        if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(m, l);
+    }
+};
+
+// Few units of many parts: a wave per unit, query head and 32 dimensions.
+// Eight lanes take four dimensions each, eight lane groups the parts.  One CU
+// has few enough lines under way at a time that 64 parts of 512 bytes took it
+// 4 us more than a line of each.
+template <int D>
+__global__ __launch_bounds__(64) void paged_attn_join_wide_kernel(const AttnArgs a) {
+    const int row = blockIdx.y, d = 32 * blockIdx.z + 4 * (threadIdx.x & 7), pg = threadIdx.x >> 3;
+    const Split s = split_of(a);
+    if (s.n == 0 || row >= s.u.rows) return;
+    Sum x;
+    x.parts(a, s, D, row, d, pg, 8);
+#pragma unroll
+    for (int i = 8; i < 64; i <<= 1) {
+        const f32x4 v = {__shfl_xor(x.o.x, i), __shfl_xor(x.o.y, i), __shfl_xor(x.o.z, i), __shfl_xor(x.o.w, i)};
+        const float m2 = __shfl_xor(x.m, i), l2 = __shfl_xor(x.l, i);
+        x.add(v, m2, l2);
+    }
+    if (pg == 0) x.write(a, s.u, D, row, d);
+}
+
+// Many units: one work group each (its start alone costs 0.5 ns of the whole
+// device, so that one per unit, head and 32 dimensions took 12 us for 512
+// units of 8 heads).  Threads take (row, four dimensions), and where that
+// leaves some over, the parts in groups whose sums are added in order.
 template <int D>
 __global__ __launch_bounds__(256) void paged_attn_join_kernel(const AttnArgs a) {
-    constexpr int DL = D / 4, PG = 256 / DL;
-    __shared__ f32x4 sums[PG][DL];
-    __shared__ float pm[PG], pl[PG];
-    const int g = blockIdx.x, row = blockIdx.y;
-    const int2 info = a.meta[g];
-    if (info.y == 0) return;
-    const int unit = info.x - 1, n = info.y + 1;
-    const Unit u = unit_of(a, unit / a.batch, unit % a.batch);
-    if (row >= u.rows) return;
-    const int pf = part_floats(a.heads_per_block, D);
-    const int tid = threadIdx.x, pg = tid / DL, d = 4 * (tid % DL);
-    auto part = [&](int p) { return a.parts + (int64_t)(2 * (g + p) + (p == 0 ? 1 : 0)) * pf; };
-    if (pg < PG) {
-        f32x4 o = {0, 0, 0, 0};
-        float m = -INFINITY, l = 0.0f;
-        for (int p = pg; p < n; p += PG) {
-            const float* at = part(p);
-            const f32x4 v = *(const f32x4*)(at + row * D + d);
-            const float m2 = at[a.heads_per_block * D + 2 * row], l2 = at[a.heads_per_block * D + 2 * row + 1];
-            const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.0f : top;
-            const float f = __builtin_amdgcn_exp2f(m - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
-            o = o * f + v * f2;
-            l = l * f + l2 * f2;
-            m = top;
+    constexpr int DL = D / 4;
+    __shared__ f32x4 so[256];
+    __shared__ f32x2 sml[256];
+    const Split s = split_of(a);
+    if (s.n == 0) return;
+    const int tid = threadIdx.x, items = s.u.rows * DL;
+    for (int base = 0; base < items; base += 256) {
+        const int span = items - base < 256 ? items - base : 256;
+        int groups = 256 / span;
+        if (groups > s.n) groups = s.n;
+        const int pg = tid / span, item = base + tid % span, row = item / DL, d = 4 * (item % DL);
+        Sum x;
+        if (pg < groups) x.parts(a, s, D, row, d, pg, groups);
+        if (groups > 1) {
+            so[tid] = x.o;
+            sml[tid] = f32x2{x.m, x.l};
+            __syncthreads();
+            if (pg == 0)
+                for (int p = 1; p < groups; ++p) x.add(so[p * span + tid], sml[p * span + tid].x, sml[p * span + tid].y);
+            __syncthreads();
         }
-        sums[pg][tid % DL] = o;
-        if (d == 0) {
-            pm[pg] = m;
-            pl[pg] = l;
-        }
+        if (pg == 0) x.write(a, s.u, D, row, d);
     }
-    __syncthreads();
-    if (tid >= DL) return;
-    float top = -INFINITY;
-    for (int p = 0; p < PG; ++p) top = fmaxf(top, pm[p]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    f32x4 o = {0, 0, 0, 0};
-    float l = 0.0f;
-    for (int p = 0; p < PG; ++p) {
-        const float f = __builtin_amdgcn_exp2f(pm[p] - base);
-        o += sums[p][tid] * f;
-        l += pl[p] * f;
-    }
-    *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * D + d) = o * (1.0f / l);
-    if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l);
 }
 
 template <int KIND, int NB>
@@ -633,10 +701,16 @@ void launch(const AttnArgs& a, hipStream_t st) {
     const size_t lds = (size_t)8 * part_floats(a.heads_per_block, 32 * NB) * sizeof(float);
     if (lds > 64 * 1024)
         (void)hipFuncSetAttribute((const void*)paged_attn_kernel<KIND, NB>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    paged_attn_kernel<KIND, NB><<<dim3((unsigned)a.groups), 256, lds, st>>>(a);
-    if (a.groups > 1)
-        paged_attn_join_kernel<32 * NB><<<dim3((unsigned)a.groups, (unsigned)a.heads_per_block), 256, 0, st>>>(a);
+    const dim3 grid = a.per_unit ? dim3((unsigned)a.batch, (unsigned)a.head_spaces) : dim3((unsigned)a.groups);
+    paged_attn_kernel<KIND, NB><<<grid, 256, lds, st>>>(a);
+    if (a.per_unit) return;
+    const int64_t units = a.head_spaces * a.batch;
+    if (units * 8 <= a.groups)
+        paged_attn_join_wide_kernel<32 * NB><<<dim3((unsigned)units, (unsigned)a.heads_per_block, NB), 64, 0, st>>>(a);
+    else
+        paged_attn_join_kernel<32 * NB><<<dim3((unsigned)(a.meta_by_unit ? units : a.groups)), 256, 0, st>>>(a);
 }
+
 
 template <int KIND>
 void launch_kind(const AttnArgs& a, int head_dim, hipStream_t st) {
@@ -664,10 +738,18 @@ AttnPlan plan_paged_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t 
     const int64_t tiles = (capacity + TILE - 1) / TILE;
     const int64_t most = (batch * tiles * p.head_spaces + 3) / 4;
     const int64_t want = (int64_t)num_cu * 2;
+    // Short tables: a work group per unit saves the scan of the lengths and the
+    // join (8 kv heads of 128, 4 query heads each, f16, one sequence: 32 tokens
+    // 4.1 us against 6.7, 256 tokens 7.3 / 9.1, 512 tokens 10.8 / 10.4, 1024
+    // tokens 16.3 / 9.9; 64 sequences of 512 27.7 / 30.6), as long as the units
+    // are not many more than fit the device at a time (256 sequences of 32:
+    // 18.4 us against 14.9).
+    p.per_unit = tiles <= 16 && batch * p.head_spaces <= 4 * (int64_t)num_cu;
     p.groups = (int)(most < want ? most : want);
+    p.meta_by_unit = batch * p.head_spaces <= p.groups;
     p.meta_bytes = ((int64_t)p.groups * 8 + 255) / 256 * 256;
     const int64_t part = (int64_t)part_floats(p.heads_per_block, (int)head_dim) * 4;
-    p.ws_bytes = p.groups > 1 ? p.meta_bytes + (2 * p.groups * part + 255) / 256 * 256 : 0;
+    p.ws_bytes = !p.per_unit ? p.meta_bytes + (2 * p.groups * part + 255) / 256 * 256 : 0;
     return p;
 }
 

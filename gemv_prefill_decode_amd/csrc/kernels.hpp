@@ -206,6 +206,8 @@ void launch_kv_append(const AppendArgs& a, int kind, int head_dim, hipStream_t s
 // (head space, sequence, tile).
 struct AttnPlan {
     int blocks_per_kv, heads_per_block, groups;
+    bool per_unit;                 // a work group per (head space, sequence) instead
+    bool meta_by_unit;             // the joins are listed by unit, not by work group
     int64_t head_spaces;
     int64_t meta_bytes, ws_bytes;  // workspace: meta, then two parts per group
 };
@@ -225,7 +227,9 @@ struct AttnArgs {
     const int* lens;
     int batch, n_q, group, capacity;
     int blocks_per_kv, heads_per_block, groups;
+    bool per_unit, meta_by_unit;
     int64_t head_spaces;
+    double inv_groups;
     float scale_log2e;
     int2* meta;
     float* parts;

@@ -13,12 +13,9 @@ namespace {
 // row R + r (R = sum of n before it): position c + r, slot = page of the position * P + its place.
 // A few thousand integers: launch and memory latency bound it.  One kernel
 // without communication between work groups: each scans all sequences in
-// passes of EXT_THREADS (two sums), and writes its own range of rows and its
+// passes of THREADS (two sums), and writes its own range of rows and its
 // stride of new table entries, which it finds in the pass by bisection.
-constexpr int EXT_THREADS = 1024;
-constexpr int EXT_ROWS = 4096;  // rows per work group
-
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ T block_inclusive(T v, T* waves, T* total) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
@@ -29,7 +26,7 @@ __device__ __forceinline__ T block_inclusive(T v, T* waves, T* total) {
     if (lane == 63) waves[w] = v;
     __syncthreads();
     T t = 0;
-    for (int i = 0; i < EXT_THREADS / 64; ++i) {
+    for (int i = 0; i < THREADS / 64; ++i) {
         if (i < w) v += waves[i];
         t += waves[i];
     }
@@ -38,9 +35,9 @@ __device__ __forceinline__ T block_inclusive(T v, T* waves, T* total) {
 }
 
 // First index whose inclusive sum exceeds x (sums do not decrease).
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ int bisect(const T* sums, T x) {
-    int lo = 0, hi = EXT_THREADS - 1;
+    int lo = 0, hi = THREADS - 1;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (sums[mid] > x)
@@ -51,27 +48,28 @@ __device__ __forceinline__ int bisect(const T* sums, T x) {
     return lo;
 }
 
-__global__ __launch_bounds__(EXT_THREADS) void paged_extend_kernel(const ExtendArgs a) {
-    __shared__ int64_t row_end[EXT_THREADS], row_waves[EXT_THREADS / 64];
-    __shared__ int need_end[EXT_THREADS], need_waves[EXT_THREADS / 64];
-    __shared__ int cached[EXT_THREADS], fresh[EXT_THREADS];
-    __shared__ bool taken[EXT_THREADS];
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void paged_extend_kernel(const ExtendArgs a, int rows_per_group) {
+    __shared__ int64_t row_end[THREADS], row_waves[THREADS / 64];
+    __shared__ int need_end[THREADS], need_waves[THREADS / 64];
+    __shared__ int cached[THREADS], fresh[THREADS];
+    __shared__ bool taken[THREADS];
     const int tid = threadIdx.x;
-    const int64_t lo = (int64_t)blockIdx.x * EXT_ROWS;
-    const int64_t hi = lo + EXT_ROWS < a.n_rows ? lo + EXT_ROWS : a.n_rows;
+    const int64_t lo = (int64_t)blockIdx.x * rows_per_group;
+    const int64_t hi = lo + rows_per_group < a.n_rows ? lo + rows_per_group : a.n_rows;
     const int mask = (1 << a.page_log2) - 1;
     auto pages = [&](int64_t tokens) { return (int)((tokens + mask) >> a.page_log2); };
     int64_t rows_before = 0;
     int need_before = 0;
-    for (int base = 0, pass = 0; base < a.batch; base += EXT_THREADS, ++pass) {
+    for (int base = 0, pass = 0; base < a.batch; base += THREADS, ++pass) {
         const int b = base + tid;
         const int c = b < a.batch ? a.cached[b] : 0, n = b < a.batch ? a.fresh[b] : 0;
         bool ok = c >= 0 && n >= 0 && (int64_t)c + n <= a.capacity;
         const int need = ok ? pages((int64_t)c + n) - pages(c) : 0;
         int64_t rows_total;
         int need_total;
-        const int64_t rows_incl = rows_before + block_inclusive<int64_t>(n > 0 ? n : 0, row_waves, &rows_total);
-        const int need_incl = need_before + block_inclusive<int>(need, need_waves, &need_total);
+        const int64_t rows_incl = rows_before + block_inclusive<THREADS, int64_t>(n > 0 ? n : 0, row_waves, &rows_total);
+        const int need_incl = need_before + block_inclusive<THREADS, int>(need, need_waves, &need_total);
         ok = ok && (need == 0 || need_incl <= a.n_free);
         row_end[tid] = rows_incl;
         need_end[tid] = need_incl;
@@ -82,17 +80,17 @@ __global__ __launch_bounds__(EXT_THREADS) void paged_extend_kernel(const ExtendA
         __syncthreads();
 
         // new table entries
-        for (int e = need_before + blockIdx.x * EXT_THREADS + tid; e < need_before + need_total && e < a.n_free;
-             e += gridDim.x * EXT_THREADS) {
-            const int s = bisect(need_end, e);
+        for (int e = need_before + blockIdx.x * THREADS + tid; e < need_before + need_total && e < a.n_free;
+             e += gridDim.x * THREADS) {
+            const int s = bisect<THREADS>(need_end, e);
             const int begin = s ? need_end[s - 1] : need_before;
             if (taken[s]) a.table[(int64_t)(base + s) * a.table_stride + pages(cached[s]) + (e - begin)] = a.free_pages[e];
         }
         // this work group's rows that belong to the pass
         const int64_t r_lo = lo > rows_before ? lo : rows_before;
         const int64_t r_hi = hi < rows_before + rows_total ? hi : rows_before + rows_total;
-        for (int64_t r = r_lo + tid; r < r_hi; r += EXT_THREADS) {
-            const int s = bisect(row_end, r);
+        for (int64_t r = r_lo + tid; r < r_hi; r += THREADS) {
+            const int s = bisect<THREADS>(row_end, r);
             const int pos = (int)(cached[s] + (r - (row_end[s] - fresh[s])));
             int slot = -1;
             if (taken[s]) {
@@ -109,7 +107,7 @@ __global__ __launch_bounds__(EXT_THREADS) void paged_extend_kernel(const ExtendA
         need_before += need_total;
         __syncthreads();
     }
-    for (int64_t r = (lo > rows_before ? lo : rows_before) + tid; r < hi; r += EXT_THREADS) {
+    for (int64_t r = (lo > rows_before ? lo : rows_before) + tid; r < hi; r += THREADS) {
         a.slots[r] = -1;
         a.positions[r] = -1;
     }
@@ -211,9 +209,16 @@ void append_kind(const AppendArgs& a, int head_dim, hipStream_t st) {
 }  // namespace
 
 void launch_paged_extend(const ExtendArgs& a, hipStream_t st) {
-    int64_t groups = ((int64_t)a.n_rows + EXT_ROWS - 1) / EXT_ROWS;
+    // a row per thread, in at most 512 work groups (each scans all sequences)
+    const int threads = a.batch <= 256 ? 256 : 1024;
+    int64_t rows = ((int64_t)a.n_rows + 511) / 512;
+    if (rows < threads) rows = threads;
+    int64_t groups = ((int64_t)a.n_rows + rows - 1) / rows;
     if (groups < 1) groups = 1;
-    paged_extend_kernel<<<dim3((unsigned)groups), EXT_THREADS, 0, st>>>(a);
+    if (threads == 256)
+        paged_extend_kernel<256><<<dim3((unsigned)groups), 256, 0, st>>>(a, (int)rows);
+    else
+        paged_extend_kernel<1024><<<dim3((unsigned)groups), 1024, 0, st>>>(a, (int)rows);
 }
 
 void launch_kv_append(const AppendArgs& a, int kind, int head_dim, hipStream_t st) {

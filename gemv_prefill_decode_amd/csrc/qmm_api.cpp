@@ -946,6 +946,9 @@ int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int
     a.blocks_per_kv = pl.blocks_per_kv;
     a.heads_per_block = pl.heads_per_block;
     a.groups = pl.groups;
+    a.per_unit = pl.per_unit;
+    a.meta_by_unit = pl.meta_by_unit;
+    a.inv_groups = 1.0 / pl.groups;
     a.head_spaces = pl.head_spaces;
     a.scale_log2e = scale * 1.4426950408889634f;
     a.meta = pl.ws_bytes > 0 ? (int2*)workspace : nullptr;

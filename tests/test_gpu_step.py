@@ -345,9 +345,9 @@ def test_attention_shared_pages_strided_rows_and_own_workspace():
     wide = torch.zeros(3, 8 * 64 + 100, device="cuda")
     wide[:, 4:4 + 512] = c["q"].flatten(1)
     out = torch.full((3, 8 * 64 + 60), 5.0, device="cuda")
-    tab = torch.full((3, 40), -9, dtype=torch.int32, device="cuda")
+    tab = torch.full((3, 600), -9, dtype=torch.int32, device="cuda")
     tab[:, 5:5 + c["table"].shape[1]] = torch.from_numpy(c["table"]).cuda()
-    tab = tab[:, 5:5 + c["table"].shape[1]]
+    tab = tab[:, 5:505]                     # room for 8000 tokens: the split is made for those
     lens = torch.tensor(c["lens"], dtype=torch.int32, device="cuda")
     need = qmm.paged_attention_workspace_bytes(3, 8, c["cache"], tab.shape[1])
     ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")     # any contents
