@@ -44,6 +44,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int TILE = 32;      // tokens per wave step
 constexpr int HEADS = 16;     // query heads per pass over a unit's rows
+// Work groups per CU that the registers are shared between.  Two hold 128 KB
+// (8-bit: 64 KB) of loads in flight on a CU, and more read no faster: with
+// three or four, where the registers allow it, 8-bit heads of 128 went from
+// 103 to 121 us and f16 heads of 64 from 92 to 97 us (64 sequences of 4096).
+constexpr int occupancy(int kind, int nb) { return nb <= (kind == KV_Q8 ? 6 : 5) ? 2 : 1; }
 constexpr float PBITS = 14.0f;
 constexpr float P_UNIT = 6.103515625e-05f;  // 2^-14
 constexpr float LN2 = 0.6931471805599453f;
@@ -55,14 +60,29 @@ __device__ __forceinline__ float from_lane(float v, int lane) {
     return fbits(__builtin_amdgcn_ds_bpermute(4 * lane, (int)ubits(v)));
 }
 
-// The maximum (sum) over the four lanes that differ in lane / 16.
+// The maximum (sum) over the four lanes that differ in lane / 16, in each of
+// them: row exchanges (v_permlane16_swap, v_permlane32_swap), no LDS.
+__device__ __forceinline__ void swap16(float v, float* x, float* y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(ubits(v), ubits(v), false, false);
+    *x = fbits(r[0]);
+    *y = fbits(r[1]);
+}
+__device__ __forceinline__ void swap32(float v, float* x, float* y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(ubits(v), ubits(v), false, false);
+    *x = fbits(r[0]);
+    *y = fbits(r[1]);
+}
 __device__ __forceinline__ float max_c(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    float x, y;
+    swap16(v, &x, &y);
+    swap32(fmaxf(x, y), &x, &y);
+    return fmaxf(x, y);
 }
 __device__ __forceinline__ float sum_c(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    float x, y;
+    swap16(v, &x, &y);
+    swap32(x + y, &x, &y);
+    return x + y;
 }
 
 // Tokens of a sequence: -1 for a length the table cannot hold (its outputs
@@ -74,18 +94,23 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
 // A unit without tokens still takes one tile, whose wave writes its outputs.
 __device__ __forceinline__ int seq_tiles(int len) { return len <= TILE ? 1 : (len + TILE - 1) / TILE; }
 
-template <int N>
+template <bool NT, typename T>
+__device__ __forceinline__ T ldx(const char* p) {
+    if constexpr (NT) return __builtin_nontemporal_load((const T*)p);
+    return *(const T*)p;
+}
+template <bool NT, int N>
 __device__ __forceinline__ void ldg(uint32_t (&dst)[N], int at, const char* p, int bytes) {
     if (bytes == 16) {
-        const u32x4 v = *(const u32x4*)p;
+        const u32x4 v = ldx<NT, u32x4>(p);
         dst[at] = v.x; dst[at + 1] = v.y; dst[at + 2] = v.z; dst[at + 3] = v.w;
     } else if (bytes == 8) {
-        const u32x2 v = *(const u32x2*)p;
+        const u32x2 v = ldx<NT, u32x2>(p);
         dst[at] = v.x; dst[at + 1] = v.y;
     } else if (bytes == 4) {
-        dst[at] = *(const uint32_t*)p;
+        dst[at] = ldx<NT, uint32_t>(p);
     } else {
-        dst[at] = *(const uint16_t*)p;
+        dst[at] = ldx<NT, uint16_t>(p);
     }
 }
 
@@ -155,30 +180,58 @@ struct Segment {
     float m, l;
     float vexp;      // 8-bit values: acc holds sums divided by this power of two
 
-    static __device__ __forceinline__ void load_k(uint32_t (&kr)[KW], const char* row, int c) {
-        if constexpr (Q8) {
+    // Rows of whole lines are read once and past the caches (non-temporal: 131071
+    // tokens of f16 heads of 128 94.9 -> 91.1 us); rows that share lines are not
+    // (2048 tokens x 64 of 8-bit heads of 96: 63 us, non-temporal 84).
+    static constexpr bool STREAM = D * ES % 128 == 0;
+
+    // A key row's 128-byte lines, then what is left: 64 and 32 bytes.
+    static constexpr int LINES = D * ES / 128;
+    static constexpr bool REST64 = (D * ES & 64) != 0, REST32 = (D * ES & 32) != 0;
+
+    // The lane's share of 16 rows: row i (its operand row), which needs the
+    // 16-byte chunks 2c and 2c + 1 of every line.  A load instruction takes
+    // whole lines, of eight rows: even and odd lanes read chunk 2c and 2c + 1
+    // first of the even row, then of the odd one (odd: rows of the pair), and
+    // settle() swaps what the other one needs.
+    static __device__ __forceinline__ void load_k(uint32_t (&kr)[KW], const char* even, const char* odd, const char* own,
+                                                  int c, int i) {
 #pragma unroll
-            for (int p = 0; p < NB / 2; ++p) ldg(kr, 4 * p, row + 64 * p + 16 * c, 16);
-            if constexpr (N2) ldg(kr, 4 * (NB / 2), row + 64 * (NB / 2) + 8 * c, 8);
-        } else {
-#pragma unroll
-            for (int s = 0; s < NB; ++s) ldg(kr, 4 * s, row + 64 * s + 16 * c, 16);
+        for (int n = 0; n < LINES; ++n) {
+            const int at = 128 * n + 32 * c + 16 * (i & 1);
+            ldg<STREAM>(kr, 8 * n, even + at, 16);
+            ldg<STREAM>(kr, 8 * n + 4, odd + at, 16);
         }
+        if constexpr (REST64) ldg<STREAM>(kr, 8 * LINES, own + 128 * LINES + 16 * c, 16);
+        if constexpr (REST32) ldg<STREAM>(kr, 8 * LINES + (REST64 ? 4 : 0), own + D * ES - 32 + 8 * c, 8);
+    }
+    static __device__ __forceinline__ void settle(uint32_t (&kr)[KW], int i) {
+        const bool odd = i & 1;
+#pragma unroll
+        for (int n = 0; n < LINES; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = kr[8 * n + j], y = kr[8 * n + 4 + j];
+                // quad_perm [1, 0, 3, 2]: the neighbour's
+                const uint32_t px = __builtin_amdgcn_update_dpp(0, x, 0xb1, 0xf, 0xf, true);
+                const uint32_t py = __builtin_amdgcn_update_dpp(0, y, 0xb1, 0xf, 0xf, true);
+                kr[8 * n + j] = odd ? py : x;
+                kr[8 * n + 4 + j] = odd ? y : px;
+            }
     }
     static __device__ __forceinline__ void load_v(uint32_t (&vr)[VW], const char* row, int i) {
 #pragma unroll
-        for (int n = 0; n < N8; ++n) ldg(vr, n * 2 * ES, row + ES * (128 * n + 8 * i), 8 * ES);
-        if constexpr (N4) ldg(vr, N8 * 2 * ES, row + ES * (128 * N8 + 4 * i), 4 * ES);
-        if constexpr (N2) ldg(vr, (N8 * 2 + (N4 ? 1 : 0)) * ES, row + ES * (128 * N8 + (N4 ? 64 : 0) + 2 * i), 2 * ES);
+        for (int n = 0; n < N8; ++n) ldg<STREAM>(vr, n * 2 * ES, row + ES * (128 * n + 8 * i), 8 * ES);
+        if constexpr (N4) ldg<STREAM>(vr, N8 * 2 * ES, row + ES * (128 * N8 + 4 * i), 4 * ES);
+        if constexpr (N2) ldg<STREAM>(vr, (N8 * 2 + (N4 ? 1 : 0)) * ES, row + ES * (128 * N8 + (N4 ? 64 : 0) + 2 * i), 2 * ES);
     }
     // first dimension of the eight that lane c's share of step s holds
     static __device__ __forceinline__ int kdim(int s, int c) {
-        if constexpr (Q8) {
-            if (N2 && s == NB - 1) return 32 * s + 8 * c;
-            return 64 * (s / 2) + 16 * c + 8 * (s % 2);
-        } else {
-            return 32 * s + 8 * c;
-        }
+        constexpr int CH = 16 / ES, PER = 32 / ES / 8;  // dimensions in a chunk; steps of a line
+        if (s < PER * LINES) return 128 / ES * (s / PER) + 2 * CH * c + 8 * (s % PER);
+        s -= PER * LINES;
+        if (REST64 && s < PER / 2) return 128 / ES * LINES + CH * c + 8 * s;
+        return D - 32 + 8 * c;  // 32 bytes: 8-bit rows
     }
     // the key operand of step s
     static __device__ __forceinline__ u32x4 key(const uint32_t (&kr)[KW], int s) {
@@ -248,7 +301,9 @@ struct Segment {
         uint32_t kr[2][KW], vr[8][VW];
         auto load_keys = [&]() {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) load_k(kr[h], row_of(kb, 16 * h + i), c);
+            for (int h = 0; h < 2; ++h)
+                load_k(kr[h], row_of(kb, 16 * h + (i & ~1)), row_of(kb, 16 * h + (i | 1)),
+                       REST64 || REST32 ? row_of(kb, 16 * h + i) : kb, c, i);
         };
         auto tok_of = [&](int j) { return (j < 4 ? 0 : 12) + 4 * c + j; };  // token of the lane's k index j
         auto load_values = [&]() {
@@ -296,6 +351,8 @@ struct Segment {
             const int tt = t + it;
             const bool more = it + 1 < n;
             f32x4 s4[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+            settle(kr[0], i);
+            settle(kr[1], i);
 #pragma unroll
             for (int s = 0; s < NB; ++s)
 #pragma unroll
@@ -482,7 +539,7 @@ __device__ __forceinline__ int64_t cut(const AttnArgs& a, int g, int w, int64_t*
 }
 
 template <int KIND, int NB>
-__global__ __launch_bounds__(256, NB <= 4 ? 2 : 1) void paged_attn_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(const AttnArgs a) {
     constexpr int D = 32 * NB;
     extern __shared__ __attribute__((aligned(16))) float parts[];  // [wave][2] parts
     __shared__ int part_unit[4][2], part_ends[4][2];
