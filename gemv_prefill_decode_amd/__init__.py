@@ -654,16 +654,24 @@ def _table(torch, t, dev, batch):
     return _refuse(t, "block_table", torch.int32, dev, f"[{batch}, max_pages] with contiguous rows")
 
 
-def _call(torch, dev, name, *args, stream):
+def _call(torch, dev, f, args, stream):
     """A library call on device dev, on the given stream or the device's current one."""
-    f = getattr(_LIB, name)
     if torch._C._cuda_getDevice() == dev:
         st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
             st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if st != 0:
-        raise QmmError(st, name)
+        raise QmmError(st, f.__name__)
+
+
+def _new(torch, shape, dtype, like, stream):
+    """An output (or workspace) on like's device, allocated on the stream that writes it: memory of
+    another stream may still be read there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _device_of(torch, t, what):
@@ -681,27 +689,28 @@ def paged_extend(block_table, cached_lens, new_lens, free_pages, page_size: int,
     after sequence, -1 behind the last row and (slots) for a sequence that is refused because its
     table row or the free list is too short: its seq_lens entry stays cached_lens."""
     import torch
-    load()
+    lib = _LIB or load()
     dev = _device_of(torch, block_table, "block_table")
     i32 = torch.int32
     batch = cached_lens.shape[0]
     n_free = free_pages.numel()
     table, max_pages, ld = _table(torch, block_table, dev, batch)
     if seq_lens is None:
-        seq_lens = torch.empty(batch, dtype=i32, device=block_table.device)
+        seq_lens = _new(torch, batch, i32, block_table, stream)
     if slots is None:
-        slots = torch.empty(n_rows, dtype=i32, device=block_table.device)
+        slots = _new(torch, n_rows, i32, block_table, stream)
     if positions is None:
-        positions = torch.empty(n_rows, dtype=i32, device=block_table.device)
+        positions = _new(torch, n_rows, i32, block_table, stream)
     if pages_used is None:
-        pages_used = torch.empty(1, dtype=i32, device=block_table.device)
+        pages_used = _new(torch, 1, i32, block_table, stream)
     one, rows = (batch,), (n_rows,)
-    _call(torch, dev, "qmm_paged_extend", table, ld, _packed(torch, seq_lens, "seq_lens", i32, dev, one),
-          _packed(torch, slots, "slots", i32, dev, rows), _packed(torch, positions, "positions", i32, dev, rows),
-          _packed(torch, pages_used, "pages_used", i32, dev, (1,)),
-          _packed(torch, cached_lens, "cached_lens", i32, dev, one), _packed(torch, new_lens, "new_lens", i32, dev, one),
-          _packed(torch, free_pages, "free_pages", i32, dev, (n_free,)), batch, max_pages, page_size, n_free, n_rows,
-          stream=stream)
+    args = (table, ld, _packed(torch, seq_lens, "seq_lens", i32, dev, one),
+            _packed(torch, slots, "slots", i32, dev, rows), _packed(torch, positions, "positions", i32, dev, rows),
+            _packed(torch, pages_used, "pages_used", i32, dev, (1,)),
+            _packed(torch, cached_lens, "cached_lens", i32, dev, one),
+            _packed(torch, new_lens, "new_lens", i32, dev, one),
+            _packed(torch, free_pages, "free_pages", i32, dev, (n_free,)), batch, max_pages, page_size, n_free, n_rows)
+    _call(torch, dev, lib.qmm_paged_extend, args, stream)
     return seq_lens, slots, positions, pages_used
 
 
@@ -710,12 +719,12 @@ def kv_append(cache: KVCache, k, v, slots, stream=None):
     stride apart, as views of a fused projection's output) into their slots (int32 [n]; a slot
     outside the cache, such as -1, is skipped; the others must differ)."""
     import torch
-    load()
+    lib = _LIB or load()
     dev, row, heads = cache._index, cache._row, cache.n_kv
     n = slots.shape[0]
-    _call(torch, dev, "qmm_kv_append", cache._ptr, *_f32_rows(torch, k, "k", dev, n, row, heads),
-          *_f32_rows(torch, v, "v", dev, n, row, heads), _packed(torch, slots, "slots", torch.int32, dev, (n,)), n,
-          stream=stream)
+    args = (cache._ptr, *_f32_rows(torch, k, "k", dev, n, row, heads), *_f32_rows(torch, v, "v", dev, n, row, heads),
+            _packed(torch, slots, "slots", torch.int32, dev, (n,)), n)
+    _call(torch, dev, lib.qmm_kv_append, args, stream)
 
 
 def paged_attention_workspace_bytes(batch: int, n_q: int, cache: KVCache, max_pages: int) -> int:
@@ -738,14 +747,14 @@ def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=No
     for the call, from the graph's own memory under capture) or a device tensor of at least
     paged_attention_workspace_bytes() bytes that no other call uses at the same time."""
     import torch
-    lib = load()
+    lib = _LIB or load()
     dev, d = cache._index, cache.head_dim
     batch = seq_lens.shape[0]
     n_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
     row = n_q * d
     qp, ldq = _f32_rows(torch, q, "q", dev, batch, row, n_q)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        out = _new(torch, q.shape, torch.float32, q, stream)
     op, ldo = _f32_rows(torch, out, "out", dev, batch, row, n_q)
     table, max_pages, ld = _table(torch, block_table, dev, batch)
     lp = None if lse is None else _packed(torch, lse, "lse", torch.float32, dev, (batch, n_q))
@@ -760,19 +769,16 @@ def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=No
             else:
                 ws_len = paged_attention_workspace_bytes(batch, n_q, cache, max_pages)
             if ws_len > 0:
-                if stream is None:
-                    workspace = torch.empty(ws_len, dtype=torch.uint8, device=cache.device)
-                else:
-                    with torch.cuda.stream(stream):     # memory of the stream that uses it
-                        workspace = torch.empty(ws_len, dtype=torch.uint8, device=cache.device)
+                workspace = _new(torch, ws_len, torch.uint8, q, stream)
                 ws = workspace.data_ptr()
             else:
                 ws_len = 0
         else:
             ws_len = workspace.numel() * workspace.element_size()
             ws = _packed(torch, workspace, "workspace", workspace.dtype, dev, workspace.shape)
-    _call(torch, dev, "qmm_paged_attention", op, ldo, lp, qp, ldq, cache._ptr, table, ld, lens, batch, n_q, max_pages,
-          d ** -0.5 if scale is None else scale, ws, ws_len, stream=stream)
+    args = (op, ldo, lp, qp, ldq, cache._ptr, table, ld, lens, batch, n_q, max_pages,
+            d ** -0.5 if scale is None else scale, ws, ws_len)
+    _call(torch, dev, lib.qmm_paged_attention, args, stream)
     return out
 
 
@@ -781,17 +787,18 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-5, y=None, h=None, str
     unless a tensor is given for it) and y = h * weight / sqrt(mean(h*h) + eps), float32 [n, k],
     k a multiple of 4.  Rows of any of them may be any multiple of 4 apart."""
     import torch
-    load()
+    lib = _LIB or load()
     dev = _device_of(torch, x, "x")
     n, k = x.shape
     if y is None:
-        y = torch.empty((n, k), dtype=torch.float32, device=x.device)
+        y = _new(torch, (n, k), torch.float32, x, stream)
     if h is None and residual is not None:
-        h = torch.empty((n, k), dtype=torch.float32, device=x.device)
-    _call(torch, dev, "qmm_add_rmsnorm", *_f32_rows(torch, y, "y", dev, n, k),
-          *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)), *_f32_rows(torch, x, "x", dev, n, k),
-          *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
-          _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps, stream=stream)
+        h = _new(torch, (n, k), torch.float32, x, stream)
+    args = (*_f32_rows(torch, y, "y", dev, n, k), *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)),
+            *_f32_rows(torch, x, "x", dev, n, k),
+            *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
+            _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps)
+    _call(torch, dev, lib.qmm_add_rmsnorm, args, stream)
     return y, h
 
 
@@ -799,18 +806,19 @@ def add_rmsnorm_q8(x, weight, residual=None, eps: float = 1e-5, q=None, d=None, 
     """add_rmsnorm with y as Q8_1 activations; returns (q int8 [n, k], d float32 [n, k/32], h), q
     and d as moe_gateup_q8 takes them.  k a multiple of 32."""
     import torch
-    load()
+    lib = _LIB or load()
     dev = _device_of(torch, x, "x")
     n, k = x.shape
     if q is None:
-        q = torch.empty((n, k), dtype=torch.int8, device=x.device)
+        q = _new(torch, (n, k), torch.int8, x, stream)
     if d is None:
-        d = torch.empty((n, k // 32), dtype=torch.float32, device=x.device)
+        d = _new(torch, (n, k // 32), torch.float32, x, stream)
     if h is None and residual is not None:
-        h = torch.empty((n, k), dtype=torch.float32, device=x.device)
-    _call(torch, dev, "qmm_add_rmsnorm_q8", _packed(torch, q, "q", torch.int8, dev, (n, k)),
-          _packed(torch, d, "d", torch.float32, dev, (n, k // 32)),
-          *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)), *_f32_rows(torch, x, "x", dev, n, k),
-          *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
-          _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps, stream=stream)
+        h = _new(torch, (n, k), torch.float32, x, stream)
+    args = (_packed(torch, q, "q", torch.int8, dev, (n, k)),
+            _packed(torch, d, "d", torch.float32, dev, (n, k // 32)),
+            *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)), *_f32_rows(torch, x, "x", dev, n, k),
+            *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
+            _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps)
+    _call(torch, dev, lib.qmm_add_rmsnorm_q8, args, stream)
     return q, d, h

@@ -248,6 +248,6 @@ struct NormArgs {
     int k;
     float eps, inv_k;
 };
-void launch_add_rmsnorm(const NormArgs& a, hipStream_t st);
+void launch_add_rmsnorm(const NormArgs& a, int num_cu, hipStream_t st);
 
 }  // namespace qmm

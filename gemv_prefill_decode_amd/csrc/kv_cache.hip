@@ -122,7 +122,12 @@ __global__ __launch_bounds__(THREADS) void paged_extend_kernel(const ExtendArgs 
 // head_dim / 8 is none, which find the row's largest magnitude together.
 constexpr int APP_THREADS = 256;
 
-template <int KIND, int NB>
+template <bool NT>
+__device__ __forceinline__ f32x4 ld(const f32x4* p) {
+    return NT ? __builtin_nontemporal_load(p) : *p;
+}
+
+template <int KIND, int NB, bool NT>
 __global__ __launch_bounds__(APP_THREADS) void kv_append_kernel(const AppendArgs a) {
     constexpr int VEC = 4 * NB;  // threads' shares of a row
     constexpr int LANES = KIND != KV_Q8 ? VEC : NB == 1 ? 4 : NB == 2 ? 8 : NB <= 4 ? 16 : 32;
@@ -137,13 +142,13 @@ __global__ __launch_bounds__(APP_THREADS) void kv_append_kernel(const AppendArgs
         const int64_t tok = rows <= UINT32_MAX ? (uint32_t)row / (uint32_t)a.n_kv : row / a.n_kv;
         const int head = (int)(row - tok * a.n_kv);
         const int slot = a.slots[tok];
-        const bool live = e < VEC && slot >= 0 && slot < a.n_slots;
         f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-        if (live) {
+        if (e < VEC) {  // whether or not the row goes anywhere: the loads do not wait for its slot
             const f32x4* p = (const f32x4*)(src + tok * src_stride + (int64_t)head * (32 * NB) + 8 * e);
-            lo = p[0];
-            hi = p[1];
+            lo = ld<NT>(p);
+            hi = ld<NT>(p + 1);
         }
+        const bool live = e < VEC && slot >= 0 && slot < a.n_slots;
         const int64_t page = slot >> a.page_log2, in_page = slot & ((1 << a.page_log2) - 1);
         const int64_t at = page * a.page_stride + head * a.head_stride + in_page * a.slot_stride + 8 * e;
         if constexpr (KIND == KV_Q8) {
@@ -189,7 +194,14 @@ void append(const AppendArgs& a, hipStream_t st) {
     const int64_t rows = a.n * a.n_kv, rpb = APP_THREADS / LANES;
     int64_t blocks = (rows + rpb - 1) / rpb;
     if (blocks > 65536) blocks = 65536;
-    kv_append_kernel<KIND, NB><<<dim3((unsigned)blocks, 2), APP_THREADS, 0, st>>>(a);
+    // Rows beyond the XCDs' L2 caches together (32 MB) are read past them: 8192
+    // tokens of 8 heads of 128 22.3 -> 20.9 us; of 8 heads of 64, which they
+    // hold, 14.4 -> 14.8 us.
+    const bool nt = rows * NB * 256 > ((int64_t)32 << 20);
+    if (nt)
+        kv_append_kernel<KIND, NB, true><<<dim3((unsigned)blocks, 2), APP_THREADS, 0, st>>>(a);
+    else
+        kv_append_kernel<KIND, NB, false><<<dim3((unsigned)blocks, 2), APP_THREADS, 0, st>>>(a);
 }
 
 template <int KIND>

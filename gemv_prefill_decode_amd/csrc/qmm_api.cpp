@@ -967,7 +967,7 @@ int qmm_add_rmsnorm(float* y, int64_t ldy, float* h, int64_t ldh, const float* x
     a.y_stride = ldy;
     const int st = norm_args(&a, h, ldh, x, ldx, residual, ldr, weight, n, k, eps, 4, ldy);
     if (st) return st;
-    qmm::launch_add_rmsnorm(a, stream);
+    qmm::launch_add_rmsnorm(a, dev_props().cu, stream);
     return launch_status();
 }
 
@@ -980,7 +980,7 @@ int qmm_add_rmsnorm_q8(int8_t* q, float* d, float* h, int64_t ldh, const float* 
     a.d = d;
     const int st = norm_args(&a, h, ldh, x, ldx, residual, ldr, weight, n, k, eps, 32, 0);
     if (st) return st;
-    qmm::launch_add_rmsnorm(a, stream);
+    qmm::launch_add_rmsnorm(a, dev_props().cu, stream);
     return launch_status();
 }
 

@@ -150,16 +150,18 @@ def test_append_is_exact(kind, layout, n, n_kv, d, page):
 
 
 # ------------------------------------------------------------------ attention
-def _case(kind, lens, n_kv, group, d, page, layout="hnd", seed=0, scale=None, q_mul=1.0, kv_mul=1.0, stale=True):
-    """Inputs of a paged attention with shuffled pages; stale table entries and unwritten rows are
-    hostile: page ids far outside the cache, NaN and infinity."""
+def _case(kind, lens, n_kv, group, d, page, layout="hnd", seed=0, scale=None, q_mul=1.0, kv_mul=1.0, stale=True,
+          tokens=0):
+    """Inputs of a paged attention with shuffled pages and room for `tokens` tokens per sequence
+    (a table for more than 512 makes the kernel split the tokens between work groups); stale table
+    entries and unwritten rows are hostile: page ids far outside the cache, NaN and infinity."""
     torch = _torch()
     rng = np.random.default_rng(seed + 17 * d + group)
     pages = [-(-n // page) for n in lens]
     n_pages = sum(pages) + 2
     cache, dense = _new_cache(kind, n_pages, n_kv, page, d, layout, fill=kv_mul, rng=rng)
     ids = rng.permutation(n_pages)
-    width = max(1, max(pages)) + 1
+    width = max(max(pages) + 1, tokens // page)
     table = rng.choice([-1, 2 ** 31 - 1, -2 ** 31, n_pages, 10 ** 6], size=(len(lens), width)).astype(np.int32)
     at, used = 0, np.zeros((n_pages, page), bool)
     for i, (p, n) in enumerate(zip(pages, lens)):
@@ -225,18 +227,30 @@ def _check(c, got=None):
 LENS = [0, 1, 2, 31, 32, 33, 64, 65, 130, 0]
 
 
+@pytest.mark.parametrize("tokens", [0, 9000])
 @pytest.mark.parametrize("d", range(32, 257, 32))
 @pytest.mark.parametrize("kind", KINDS)
-def test_attention_every_head_dim(kind, d):
-    gh.note(f"attention {kind} d={d}")
-    print("worst of the bound", _check(_case(kind, LENS, 2, 3, d, 16)))
+def test_attention_every_head_dim(kind, d, tokens):
+    gh.note(f"attention {kind} d={d} table for {tokens}")
+    print("worst of the bound", _check(_case(kind, LENS, 2, 3, d, 16, tokens=tokens)))
 
 
+@pytest.mark.parametrize("tokens", [0, 9000])
 @pytest.mark.parametrize("group", [1, 2, 4, 8, 15, 16, 17, 20, 33])
 @pytest.mark.parametrize("kind", KINDS)
-def test_attention_every_group(kind, group):
-    gh.note(f"attention {kind} group={group}")
-    _check(_case(kind, LENS, 2, group, 64, 8, "nhd"))
+def test_attention_every_group(kind, group, tokens):
+    gh.note(f"attention {kind} group={group} table for {tokens}")
+    _check(_case(kind, LENS, 2, group, 64, 8, "nhd", tokens=tokens))
+
+
+@pytest.mark.parametrize("n_kv,batch,n", [(1, 1, 1), (1, 1, 40), (3, 1, 513), (8, 7, 129), (5, 3, 1000), (8, 64, 96), (2, 600, 33),
+                                          (16, 40, 260)])
+def test_attention_joins_of_every_kind(n_kv, batch, n):
+    """From one unit over all work groups to many units per wave: a unit whole in a wave, joined in
+    a work group, and over work groups by the wide and the narrow join, at the edges of chunks."""
+    gh.note(f"attention n_kv={n_kv} batch={batch} n={n}")
+    lens = [max(0, n - 13 * (i % 5)) for i in range(batch)]
+    _check(_case("f16", lens, n_kv, 2, 32, 16, tokens=2000, seed=batch))
 
 
 @pytest.mark.parametrize("page", [1, 2, 4, 8, 16, 32, 64, 128, 512])
@@ -269,9 +283,9 @@ def test_attention_many_short_sequences(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("q_mul,kv_mul", [(1e-20, 1.0), (30.0, 1.0), (1.0, 1e-4), (1e4, 1e-4), (1e-3, 1e3), (0.0, 1.0)])
+@pytest.mark.parametrize("q_mul,kv_mul", [(1e-20, 1.0), (30.0, 1.0), (1.0, 1e-6), (1.0, 1e-4), (1e4, 1e-6), (1e-3, 1e3), (0.0, 1.0)])
 def test_attention_magnitudes(kind, q_mul, kv_mul):
-    """Tiny and large queries and rows: operands in parts keep their bits at every magnitude, and a
+    """Tiny (f16 subnormal) and large queries and rows: operands in parts keep their bits at every magnitude, and a
     single dominating score is no overflow."""
     _check(_case(kind, [70, 33, 1000], 2, 4, 64, 16, q_mul=q_mul, kv_mul=kv_mul))
 
@@ -382,6 +396,51 @@ def test_cache_offsets_past_32_bits():
     out = qmm.paged_attention(gh.to_dev(q), cache, table, torch.tensor([500], dtype=torch.int32, device="cuda"))
     w, _, tol = step.attention(q[0], k.astype(np.float16), v.astype(np.float16), d ** -0.5)
     assert (np.abs(out[0].cpu().double().numpy() - w) <= tol).all()
+
+
+def test_outputs_made_for_another_stream():
+    """Outputs that a call allocates for a given stream belong to it: not memory whose last reader
+    may still be under way on the current one."""
+    torch, qmm = _torch(), _qmm()
+    c = _case("f16", [300, 40], 2, 4, 64, 16, tokens=4000)
+    table, lens = torch.from_numpy(c["table"]).cuda(), torch.tensor(c["lens"], dtype=torch.int32, device="cuda")
+    w = torch.ones(512, device="cuda")
+    want = qmm.paged_attention(c["q"], c["cache"], table, lens)
+    wy, wh = qmm.add_rmsnorm(want.flatten(1), w, want.flatten(1))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    big = torch.randn(4096, 4096, device="cuda")
+    for _ in range(5):
+        old = torch.full_like(want, 2.0)
+        slow = big @ big @ big                          # the current stream is busy
+        total = old.sum()                               # ... and reads `old` after that
+        del old
+        got = qmm.paged_attention(c["q"], c["cache"], table, lens, stream=side)
+        side.synchronize()
+        y, h = qmm.add_rmsnorm(got.flatten(1), w, got.flatten(1), stream=side)
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(y, wy) and torch.equal(h, wh)
+        assert float(total) == 2.0 * want.numel() and bool(torch.isfinite(slow[0, 0]))
+
+
+@pytest.mark.parametrize("kind,group,d", [("f16", 16, 256), ("q8", 3, 96), ("bf16", 20, 64)])
+def test_attention_captured_with_every_launch(kind, group, d):
+    """The largest LDS, two blocks of heads, both joins, and a short table, replayed."""
+    torch, qmm = _torch(), _qmm()
+    for lens, tokens in (([3000], 0), ([700] * 40, 0), ([60, 0, 33], 0)):
+        c = _case(kind, lens, 2, group, d, 16, tokens=tokens)
+        a = (c["q"], c["cache"], torch.from_numpy(c["table"]).cuda(), torch.tensor(c["lens"], dtype=torch.int32, device="cuda"))
+        want = qmm.paged_attention(*a)
+        out = torch.empty_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qmm.paged_attention(*a, out=out)
+        for _ in range(3):
+            out.fill_(5)
+            g.replay()
+            qmm.paged_attention(*a)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
 
 
 def test_attention_is_deterministic_on_any_stream_and_under_capture():
