@@ -10,9 +10,9 @@
 // that share it: 4 flops per element and query head on 2 (or 1) bytes, so
 // HBM bounds every group size the matrix cores keep up with.
 //
-// Precision.  q and out are f32, and the products are exact to f32: an f32
-// operand is split into f16 parts (high and low, 22 bits; for a bf16 cache
-// into three bf16 parts, 24 bits), each multiplied with the cache's own 16-bit
+// Precision.  q and out are f32, and the arithmetic is f32's: an f32 operand
+// (q, p) is split into f16 parts (high and low, 22 bits; for a bf16 cache into
+// three bf16 parts, 24 bits), each multiplied with the cache's own 16-bit
 // values on v_mfma_f32_16x16x32 into the same f32 sum.  The parts keep their
 // bits because q is scaled to [2^13, 2^14) per head and p to (0, 2^14], powers
 // of two that cancel at the end.  8-bit rows are exact as f16 codes; a key's
@@ -27,12 +27,22 @@
 // Loads of the next tile are issued as soon as the present one's registers
 // are read, page ids one tile further ahead.
 //
-// Split.  All (head, sequence) units' tiles form one axis that is cut into
-// equal chunks, one per work group and a quarter of it per wave, whatever the
-// lengths are: every work group scans the lengths itself, so no host plan or
-// length is needed.  A unit inside one wave is finished there; parts of a unit
+// Split.  All (head, sequence) units' tiles, and what a unit costs beside
+// them, form one axis that is cut into equal chunks, one per work group and a quarter of it per wave, whatever the
+// lengths are: every wave scans the lengths itself, so no host plan or length
+// is needed.  A unit inside one wave is finished there; parts of a unit
 // are joined in LDS, or, where it spans work groups, by a second kernel from
 // the workspace, always in the same order, so results do not vary between calls.
+// (Joining in the first kernel by the last of a unit's work groups was no
+// faster: release fences write back whole L2s, 171 us for 96; device-scope
+// stores and a counter took the 9 us that the second kernel had taken.)
+//
+// Measured (MI355X, 8 kv heads of 128): 131071 tokens of f16, 537 MB, 88 us
+// (6.1 TB/s; a kernel that only reads reaches 7.0); 51 sequences of up to
+// 16384 tokens of bf16, tokens outermost, 1109 MB, 190 us (5.8 TB/s); 64
+// sequences of up to 8192 8-bit tokens, 382 MB, 74 us (5.1 TB/s; vector ALUs
+// 55% busy with the codes' conversion); one sequence of 97 tokens, heads of
+// 64, 5.7 us (launch and four dependent loads).
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -49,6 +59,13 @@ constexpr int HEADS = 16;     // query heads per pass over a unit's rows
 // three or four, where the registers allow it, 8-bit heads of 128 went from
 // 103 to 121 us and f16 heads of 64 from 92 to 97 us (64 sequences of 4096).
 constexpr int occupancy(int kind, int nb) { return nb <= (kind == KV_Q8 ? 6 : 5) ? 2 : 1; }
+// What a unit's start and end cost its wave, in tiles: its loads are not ahead
+// of it, and its sums are written.  Counted where a wave has at least
+// START_MIN tiles, so that the waves with many short units are not the last
+// (64 sequences of up to 8192 8-bit tokens, sorted: 87.7 -> 72.1 us; of 0, 1,
+// 2 and 3 the second was 74.0, the last 72.7).  With few tiles the cuts would
+// only move off the units' ends.
+constexpr int UNIT_START = 2, START_MIN = 6;
 constexpr float PBITS = 14.0f;
 constexpr float P_UNIT = 6.103515625e-05f;  // 2^-14
 constexpr float LN2 = 0.6931471805599453f;
@@ -495,46 +512,52 @@ __device__ __forceinline__ int wave_inclusive(int v) {
     return v;
 }
 
-// A wave's run of tiles [pos, end) of the axis of all units' tiles, and where
-// it begins: unit (head space, sequence), tile in it.
+// A wave's run [pos, end) of the axis of all units, and where it begins: unit
+// (head space, sequence), offset in it.  A unit takes `start` places, for what
+// its start and end cost a wave, and then one per tile.
 struct Run {
     int64_t pos, end;
-    int hs, b, t;
+    int hs, b, at, start;
 };
 
 // Cuts the axis into a.groups equal chunks, a quarter per wave; *run: wave w's
-// of chunk g (*lo: the chunk's first tile).  Every wave scans the lengths by
-// itself, its lanes a run of consecutive sequences each.  Returns the tiles of
-// a chunk.
-__device__ __forceinline__ int64_t cut(const AttnArgs& a, int g, int w, int64_t* lo, Run* run) {
+// of chunk g.  Every wave scans the lengths by itself, its lanes a run of
+// consecutive sequences each.  Returns the places of a chunk.
+__device__ __forceinline__ int64_t cut(const AttnArgs& a, int g, int w, Run* run) {
     const int lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
     const int b_lo = lane * per, b_hi = b_lo + per < a.batch ? b_lo + per : a.batch;
     int mine = 0;
 #pragma unroll 8
     for (int b = b_lo; b < b_hi; ++b) mine += seq_tiles(seq_len(a, b));
-    const int incl = wave_inclusive(mine), before = incl - mine;
-    const int total = __builtin_amdgcn_readlane(incl, 63);  // tiles per head space
-    const int64_t all = (int64_t)total * a.head_spaces;
+    const int incl = wave_inclusive(mine);
+    int64_t total = __builtin_amdgcn_readlane(incl, 63);  // tiles per head space
+    const int start = total * a.head_spaces >= (int64_t)a.groups * 4 * START_MIN ? UNIT_START : 0;
+    const int64_t places = incl + (int64_t)start * b_hi;  // up to the lane's last sequence, and up to its first
+    const int64_t before = places - mine - (b_hi > b_lo ? start * (b_hi - b_lo) : 0);
+    total += (int64_t)start * a.batch;
+    const int64_t all = total * a.head_spaces;
     int64_t chunk = (int64_t)((double)(all + a.groups - 1) * a.inv_groups);
     if (chunk * a.groups < all) ++chunk;  // the product rounded across a whole number
-    chunk = (chunk + 3) & ~(int64_t)3;    // at least a tile per wave
-    *lo = g * chunk;
-    const int64_t hi = *lo + chunk < all ? *lo + chunk : all;
-    run->pos = *lo + w * (chunk >> 2);
+    chunk = (chunk + 3) & ~(int64_t)3;    // at least a place per wave
+    const int64_t lo = g * chunk, hi = lo + chunk < all ? lo + chunk : all;
+    run->start = start;
+    run->pos = lo + w * (chunk >> 2);
     run->end = run->pos + (chunk >> 2) < hi ? run->pos + (chunk >> 2) : hi;
     if (run->pos >= run->end) return chunk;
     run->hs = (int)floor_div(run->pos, total);
-    const int r = (int)(run->pos - (int64_t)run->hs * total);
-    const int src = __builtin_ctzll(__ballot(r >= before && r < incl));
-    int at = __builtin_amdgcn_readlane(before, src), b = src * per;
+    const int64_t r = run->pos - run->hs * total;
+    const int src = __builtin_ctzll(__ballot(r >= before && r < places));
+    int64_t at = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)before, src) |
+                 ((int64_t)__builtin_amdgcn_readlane((int)(before >> 32), src) << 32);
+    int b = src * per;
     if (per > 1)
         for (;; ++b) {
-            const int nt = seq_tiles(seq_len(a, b));
-            if (r < at + nt) break;
-            at += nt;
+            const int n = seq_tiles(seq_len(a, b)) + start;
+            if (r < at + n) break;
+            at += n;
         }
     run->b = b;
-    run->t = r - at;
+    run->at = (int)(r - at);
     return chunk;
 }
 
@@ -553,11 +576,11 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
         const int nt = seq_tiles(seq_len(a, g)), quarter = (nt + 3) / 4;
         run.hs = blockIdx.y;
         run.b = g;
-        run.pos = run.t = w * quarter;
+        run.start = 0;
+        run.pos = run.at = w * quarter;
         run.end = run.pos + quarter < nt ? run.pos + quarter : nt;
     } else {
-        int64_t lo;
-        chunk = cut(a, g, w, &lo, &run);
+        chunk = cut(a, g, w, &run);
     }
     if (lane < 2) part_unit[w][lane] = -1;
     if (tid == 0) out_unit = make_int2(0, 0);
@@ -565,9 +588,12 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
 
     const int pf = part_floats(a.heads_per_block, D);
     while (run.pos < run.end) {
-        const int b = uni(run.b), t = uni(run.t), hs = uni(run.hs);
+        const int b = uni(run.b), hs = uni(run.hs), at = uni(run.at);
         const int len = uni(seq_len(a, b)), nt = seq_tiles(len);
-        const int n = (int)(nt - t < run.end - run.pos ? nt - t : run.end - run.pos);
+        const int t = at > run.start ? at - run.start : 0;
+        const int64_t left = run.end - run.pos + at - run.start;  // tiles of the unit up to the run's end
+        const int n = (int)(left < nt ? left : nt) - t;
+        if (n <= 0) break;  // the run ends in the unit's first places: the next one starts it
         const Unit u = unit_of(a, hs, b);
         Segment<KIND, NB> seg;
         seg.run(a, b, len, u.kvh, u.head0, u.rows, t, n);
@@ -594,15 +620,15 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
             }
         }
         if (t == 0 && !a.per_unit) {  // work groups after this one that share the unit
-            const int follow = n == nt ? 0 : (int)floor_div(run.pos + nt - 1, chunk) - g;
+            const int follow = n == nt ? 0 : (int)floor_div(run.pos - at + run.start + nt - 1, chunk) - g;
             if (a.meta_by_unit) {
                 if (lane == 0) a.meta[hs * a.batch + b] = make_int2(g, follow);
             } else if (follow && lane == 0) {
                 out_unit = make_int2(hs * a.batch + b, follow);
             }
         }
-        run.pos += n;
-        run.t = 0;
+        run.pos += run.start + nt - at;
+        run.at = 0;
         run.b = b + 1;
         if (run.b == a.batch) {
             run.b = 0;
@@ -650,7 +676,7 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
     if (tid == 0 && !a.per_unit && !a.meta_by_unit) a.meta[g] = out_unit;
 }
 
-// The units that span work groups.  Its parts are part 1 of the work group it
+// The units that span work groups.  A unit's parts are part 1 of the work group it
 // starts in and part 0 of the following ones; meta says where and how many.
 // An entry per unit, or per work group where the units are more (a work group
 // starts at most one such unit): {work group or unit, following work groups}.

@@ -122,10 +122,12 @@ template <int THREADS, int T, int V, bool LOOP = false>
 void launch(const NormArgs& a, hipStream_t st) {
     constexpr int ROWS = THREADS / T;
     const dim3 grid((unsigned)((a.n + ROWS - 1) / ROWS));
-    // Inputs beyond the XCDs' L2 caches together (32 MB) are read past them:
-    // 2048 x 4096 24.9 -> 23.4 us, 512 x 14336 27.5 -> 21.1 us, 1000 x 4608 to
-    // Q8_1 17.2 -> 14.4 us; 512 x 4096, which they hold, 8.7 -> 9.1 us.
-    const bool nt = !LOOP && a.n * a.k * (a.r ? 8 : 4) > ((int64_t)32 << 20);
+    // Large inputs are read past the caches: from HBM 2048 x 4096 takes 23.1 us
+    // (else 24.2), 2048 x 4608 26.0 (33.8), 512 x 14336 20.5 (27.5), 2048 x 4096
+    // to Q8_1 23.5 (28.0).  Inputs that the 256 MB cache behind the L2s still
+    // holds from their producer lose by it (2048 x 4096 26.3 against 23.7, 1000
+    // x 4608 to Q8_1 15.5 against 14.8), so only those of over 48 MB.
+    const bool nt = !LOOP && a.n * a.k * (a.r ? 8 : 4) > ((int64_t)48 << 20);
     if (a.q && nt)
         add_rmsnorm_kernel<THREADS, T, V, true, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
     else if (a.q)

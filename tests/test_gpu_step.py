@@ -275,6 +275,19 @@ def test_attention_split_over_work_groups(kind, lens, n_kv, group, d):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_attention_large_ragged_batches(kind, seed):
+    """Enough tiles per wave for the split to count what a unit costs beside its tiles; empty, short
+    and long sequences in any order."""
+    rng = np.random.default_rng(seed)
+    lens = np.concatenate([rng.integers(0, 70, 40 * seed), rng.integers(1000, 6000, 24), [0, 1, 32, 64]])
+    rng.shuffle(lens)
+    c = _case(kind, lens.tolist(), 8, 2, 32, 32, seed=seed)
+    assert sum(max(1, -(-int(n) // 32)) for n in lens) * 8 > 512 * 4 * 6
+    _check(c)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_attention_many_short_sequences(kind):
     """More units than waves: a wave crosses sequences and heads, parts lie in every place."""
     rng = np.random.default_rng(5)
