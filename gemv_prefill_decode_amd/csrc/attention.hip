@@ -27,12 +27,15 @@
 // Loads of the next tile are issued as soon as the present one's registers
 // are read, page ids one tile further ahead.
 //
-// Split.  All (head, sequence) units' tiles, and what a unit costs beside
-// them, form one axis that is cut into equal chunks, one per work group and a quarter of it per wave, whatever the
-// lengths are: every wave scans the lengths itself, so no host plan or length
-// is needed.  A unit inside one wave is finished there; parts of a unit
-// are joined in LDS, or, where it spans work groups, by a second kernel from
-// the workspace, always in the same order, so results do not vary between calls.
+// Split.  A head space's units' tiles, and what a unit costs beside them, form
+// one axis that is cut into equal chunks, one per work group and a quarter of
+// it per wave, whatever the lengths are: every wave scans the lengths by
+// itself, so no host plan or length is needed.  All head spaces are cut alike,
+// so that heads whose rows lie side by side are read at the same time (8-bit
+// heads of 96, tokens outermost, which share lines: 62 us, 79 where the cuts
+// drift).  A unit inside one wave is finished there; parts of a unit are joined
+// in LDS, or, where it spans work groups, by a second kernel from the
+// workspace, always in the same order, so results do not vary between calls.
 // (Joining in the first kernel by the last of a unit's work groups was no
 // faster: release fences write back whole L2s, 171 us for 96; device-scope
 // stores and a counter took the 9 us that the second kernel had taken.)
@@ -496,10 +499,6 @@ __host__ __device__ __forceinline__ int part_floats(int heads_per_block, int d) 
     return heads_per_block * d + ((2 * heads_per_block + 3) & ~3);
 }
 
-// Floor of x / y for 0 <= x < 2^53, 0 < y: a quotient just below a whole
-// number is at least 1/x below it, so rounding to 53 bits does not reach it.
-__device__ __forceinline__ int64_t floor_div(int64_t x, int64_t y) { return (int64_t)((double)x / (double)y); }
-
 // Sum over the wave's lanes up to this one: row shifts within 16 lanes, then
 // the rows' last lanes handed on (no LDS).
 __device__ __forceinline__ int wave_inclusive(int v) {
@@ -512,52 +511,49 @@ __device__ __forceinline__ int wave_inclusive(int v) {
     return v;
 }
 
-// A wave's run [pos, end) of the axis of all units, and where it begins: unit
-// (head space, sequence), offset in it.  A unit takes `start` places, for what
-// its start and end cost a wave, and then one per tile.
+// A wave's run [pos, end) of its head space's axis, and where it begins:
+// sequence, offset in it.  A unit takes `start` places, for what its start and
+// end cost a wave, and then one per tile.
 struct Run {
-    int64_t pos, end;
-    int hs, b, at, start;
+    int pos, end, b, at, start;
 };
 
-// Cuts the axis into a.groups equal chunks, a quarter per wave; *run: wave w's
-// of chunk g.  Every wave scans the lengths by itself, its lanes a run of
-// consecutive sequences each.  Returns the places of a chunk.
-__device__ __forceinline__ int64_t cut(const AttnArgs& a, int g, int w, Run* run) {
+// Cuts a head space's axis into a.cuts equal chunks, a quarter per wave; *run:
+// wave w's of chunk j.  Every wave scans the lengths by itself, its lanes a run
+// of consecutive sequences each.  Returns the places of a chunk.
+__device__ __forceinline__ int cut(const AttnArgs& a, int j, int w, Run* run) {
     const int lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
     const int b_lo = lane * per, b_hi = b_lo + per < a.batch ? b_lo + per : a.batch;
     int mine = 0;
 #pragma unroll 8
     for (int b = b_lo; b < b_hi; ++b) mine += seq_tiles(seq_len(a, b));
     const int incl = wave_inclusive(mine);
-    int64_t total = __builtin_amdgcn_readlane(incl, 63);  // tiles per head space
-    const int start = total * a.head_spaces >= (int64_t)a.groups * 4 * START_MIN ? UNIT_START : 0;
-    const int64_t places = incl + (int64_t)start * b_hi;  // up to the lane's last sequence, and up to its first
-    const int64_t before = places - mine - (b_hi > b_lo ? start * (b_hi - b_lo) : 0);
-    total += (int64_t)start * a.batch;
-    const int64_t all = total * a.head_spaces;
-    int64_t chunk = (int64_t)((double)(all + a.groups - 1) * a.inv_groups);
-    if (chunk * a.groups < all) ++chunk;  // the product rounded across a whole number
-    chunk = (chunk + 3) & ~(int64_t)3;    // at least a place per wave
-    const int64_t lo = g * chunk, hi = lo + chunk < all ? lo + chunk : all;
+    int total = __builtin_amdgcn_readlane(incl, 63);
+    const int start = total / 4 / START_MIN >= a.cuts ? UNIT_START : 0;
+    const int places = incl + start * b_hi;  // up to the lane's last sequence, and up to its first
+    const int before = places - mine - (b_hi > b_lo ? start * (b_hi - b_lo) : 0);
+    total += start * a.batch;
+    int chunk = (int)(((uint32_t)total + a.cuts - 1) / (uint32_t)a.cuts);
+    if (chunk < 4) chunk = 4;  // a place per wave
+    const int quarter = (chunk + 3) >> 2;
+    const int64_t lo = (int64_t)j * chunk, pos = lo + w * quarter;
+    int64_t end = pos + quarter < lo + chunk ? pos + quarter : lo + chunk;
+    if (end > total) end = total;
     run->start = start;
-    run->pos = lo + w * (chunk >> 2);
-    run->end = run->pos + (chunk >> 2) < hi ? run->pos + (chunk >> 2) : hi;
-    if (run->pos >= run->end) return chunk;
-    run->hs = (int)floor_div(run->pos, total);
-    const int64_t r = run->pos - run->hs * total;
-    const int src = __builtin_ctzll(__ballot(r >= before && r < places));
-    int64_t at = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)before, src) |
-                 ((int64_t)__builtin_amdgcn_readlane((int)(before >> 32), src) << 32);
-    int b = src * per;
+    run->pos = run->end = 0;
+    if (pos >= end) return chunk;
+    run->pos = (int)pos;
+    run->end = (int)end;
+    const int src = __builtin_ctzll(__ballot(run->pos >= before && run->pos < places));
+    int at = __builtin_amdgcn_readlane(before, src), b = src * per;
     if (per > 1)
         for (;; ++b) {
             const int n = seq_tiles(seq_len(a, b)) + start;
-            if (r < at + n) break;
+            if (run->pos < at + n) break;
             at += n;
         }
     run->b = b;
-    run->at = (int)(r - at);
+    run->at = run->pos - at;
     return chunk;
 }
 
@@ -570,17 +566,19 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
     const int tid = threadIdx.x, w = uni(tid >> 6), lane = tid & 63;
     const int g = blockIdx.x;
 
-    int64_t chunk = 0;
+    int chunk = 0, hs, j = 0;
     Run run;
     if (a.per_unit) {
         const int nt = seq_tiles(seq_len(a, g)), quarter = (nt + 3) / 4;
-        run.hs = blockIdx.y;
+        hs = blockIdx.y;
         run.b = g;
         run.start = 0;
         run.pos = run.at = w * quarter;
         run.end = run.pos + quarter < nt ? run.pos + quarter : nt;
     } else {
-        chunk = cut(a, g, w, &run);
+        hs = g / a.cuts;
+        j = g - hs * a.cuts;
+        chunk = cut(a, j, w, &run);
     }
     if (lane < 2) part_unit[w][lane] = -1;
     if (tid == 0) out_unit = make_int2(0, 0);
@@ -588,11 +586,11 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
 
     const int pf = part_floats(a.heads_per_block, D);
     while (run.pos < run.end) {
-        const int b = uni(run.b), hs = uni(run.hs), at = uni(run.at);
+        const int b = uni(run.b), at = uni(run.at);
         const int len = uni(seq_len(a, b)), nt = seq_tiles(len);
         const int t = at > run.start ? at - run.start : 0;
-        const int64_t left = run.end - run.pos + at - run.start;  // tiles of the unit up to the run's end
-        const int n = (int)(left < nt ? left : nt) - t;
+        const int left = run.end - run.pos + at - run.start;  // tiles of the unit up to the run's end
+        const int n = (left < nt ? left : nt) - t;
         if (n <= 0) break;  // the run ends in the unit's first places: the next one starts it
         const Unit u = unit_of(a, hs, b);
         Segment<KIND, NB> seg;
@@ -620,7 +618,7 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
             }
         }
         if (t == 0 && !a.per_unit) {  // work groups after this one that share the unit
-            const int follow = n == nt ? 0 : (int)floor_div(run.pos - at + run.start + nt - 1, chunk) - g;
+            const int follow = n == nt ? 0 : (run.pos - at + run.start + nt - 1) / chunk - j;
             if (a.meta_by_unit) {
                 if (lane == 0) a.meta[hs * a.batch + b] = make_int2(g, follow);
             } else if (follow && lane == 0) {
@@ -630,10 +628,6 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
         run.pos += run.start + nt - at;
         run.at = 0;
         run.b = b + 1;
-        if (run.b == a.batch) {
-            run.b = 0;
-            run.hs = hs + 1;
-        }
     }
     __syncthreads();
 
@@ -819,7 +813,7 @@ AttnPlan plan_paged_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t 
     p.head_spaces = n_kv * p.blocks_per_kv;
     // work groups: two per CU, or as many as the tables' tiles give a tile per wave
     const int64_t tiles = (capacity + TILE - 1) / TILE;
-    const int64_t most = (batch * tiles * p.head_spaces + 3) / 4;
+    const int64_t most = (batch * tiles + 3) / 4;
     const int64_t want = (int64_t)num_cu * 2;
     // Short tables: a work group per unit saves the scan of the lengths and the
     // join (8 kv heads of 128, 4 query heads each, f16, one sequence: 32 tokens
@@ -828,7 +822,10 @@ AttnPlan plan_paged_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t 
     // are not many more than fit the device at a time (256 sequences of 32:
     // 18.4 us against 14.9).
     p.per_unit = tiles <= 16 && batch * p.head_spaces <= 4 * (int64_t)num_cu;
-    p.groups = (int)(most < want ? most : want);
+    int64_t cuts = want / p.head_spaces;
+    if (cuts > most) cuts = most;
+    p.cuts = cuts < 1 ? 1 : (int)cuts;
+    p.groups = (int)(p.cuts * p.head_spaces);
     p.meta_by_unit = batch * p.head_spaces <= p.groups;
     p.meta_bytes = ((int64_t)p.groups * 8 + 255) / 256 * 256;
     const int64_t part = (int64_t)part_floats(p.heads_per_block, (int)head_dim) * 4;

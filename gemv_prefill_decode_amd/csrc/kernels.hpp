@@ -202,10 +202,11 @@ struct AppendArgs {
 void launch_kv_append(const AppendArgs& a, int kind, int head_dim, hipStream_t st);
 
 // Paged attention.  A head space is a kv head and a block of at most 16 of
-// the query heads that share it; groups work groups each take an equal run of
-// (head space, sequence, tile).
+// the query heads that share it; cuts work groups each take an equal run of its
+// (sequence, tile).
 struct AttnPlan {
-    int blocks_per_kv, heads_per_block, groups;
+    int blocks_per_kv, heads_per_block;
+    int cuts, groups;              // work groups per head space, and in all
     bool per_unit;                 // a work group per (head space, sequence) instead
     bool meta_by_unit;             // the joins are listed by unit, not by work group
     int64_t head_spaces;
@@ -226,10 +227,9 @@ struct AttnArgs {
     int64_t table_stride;
     const int* lens;
     int batch, n_q, group, capacity;
-    int blocks_per_kv, heads_per_block, groups;
+    int blocks_per_kv, heads_per_block, cuts, groups;
     bool per_unit, meta_by_unit;
     int64_t head_spaces;
-    double inv_groups;
     float scale_log2e;
     int2* meta;
     float* parts;

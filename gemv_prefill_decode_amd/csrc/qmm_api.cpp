@@ -384,8 +384,8 @@ int check_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t head_dim, 
     if (head_dim % 32 != 0) return QMM_ERR_K_ALIGN;
     if (head_dim > 256 || batch > (1 << 20) || n_q > 65535 || !mul_ok(max_pages, page_size, cap) || *cap > KV_TOKENS_MAX)
         return QMM_ERR_RANGE;
-    // (head space, sequence) numbers and a head space's tiles are int32
-    if (batch * n_q > INT_MAX - 1 || batch * ((*cap + 31) / 32) > INT_MAX) return QMM_ERR_RANGE;
+    // (head space, sequence) numbers and a head space's tiles, with two more per sequence, are int32
+    if (batch * n_q > INT_MAX - 1 || batch * ((*cap + 31) / 32 + 2) > INT_MAX) return QMM_ERR_RANGE;
     return QMM_OK;
 }
 
@@ -948,7 +948,7 @@ int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int
     a.groups = pl.groups;
     a.per_unit = pl.per_unit;
     a.meta_by_unit = pl.meta_by_unit;
-    a.inv_groups = 1.0 / pl.groups;
+    a.cuts = pl.cuts;
     a.head_spaces = pl.head_spaces;
     a.scale_log2e = scale * 1.4426950408889634f;
     a.meta = pl.ws_bytes > 0 ? (int2*)workspace : nullptr;

@@ -556,7 +556,12 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  *                where that is 0).  No initial contents are needed.  Calls
  *                that share one must not overlap.
  * Limits (QMM_ERR_RANGE): batch <= 2^20, n_q <= 65535, max_pages*page_size
- * <= 2^30, batch*n_q and batch*ceil(max_pages*page_size/32) below 2^31.
+ * <= 2^30, batch*n_q and batch*(ceil(max_pages*page_size/32) + 2) below 2^31.
+ * The launch depends on the sizes alone, never on the lengths: a caller that
+ * knows a bound on the lengths may pass fewer columns of a wider table
+ * (max_pages below table_stride); up to 512 tokens per row one kernel does
+ * the whole.  Up to 16 query heads per kv head share one pass over a row;
+ * n_q/n_kv above that takes one pass per 16.
  */
 int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int64_t ldq, const qmm_kv_cache* cache,
                         const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens, int64_t batch,

@@ -90,6 +90,8 @@ def test_attention_refusals():
     assert f(scale=float("nan")) == f(scale=float("inf")) == f(batch=1 << 21) == RANGE
     assert f(n_q=65536, ldo=1 << 23, ldq=1 << 23) == RANGE
     assert f(width=1 << 27, ts=1 << 27) == RANGE                    # more than 2^30 tokens per row
+    assert f(batch=64, width=1 << 26, ts=1 << 26) == RANGE          # 64 * (2^25 + 2) tiles
+    assert lib.qmm_paged_attention_workspace_bytes(63, 8, 4, 64, 1 << 26, 16) > 0
     for other in (P[5], P[0], P[1], P[6], P[7], P[8], P[9]):        # out over q, the cache, the table, ...
         assert f(out=other) == ALIAS
         if other is not P[9]:
