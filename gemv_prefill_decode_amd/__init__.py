@@ -1,7 +1,7 @@
 """gemv_prefill_decode_amd - dequant-fused projection matmul for MI355X (gfx950).
 
-A thin ctypes binding over ``libqmm.so`` (the C-ABI declared in
-``include/qmm.h``).  Every step of the computation runs in the library's HIP
+A thin binding over ``libqmm.so`` (the C-ABI declared in ``include/qmm.h``):
+ctypes, and for a decode step's small calls the ``_step`` module.  Every step of the computation runs in the library's HIP
 kernels; this module only checks tensor dtypes/devices and passes data
 pointers and the current HIP stream.  PyTorch is used for device memory and
 streams.
@@ -590,7 +590,6 @@ class KVCache:
             k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
             None if v_scale is None else v_scale.data_ptr(), *k.shape, *strides, *scale_strides, KV_KINDS[self.kind])
         self._ptr = ctypes.addressof(self._struct)
-        self._row = self.n_kv * self.head_dim
 
 
 def _view_strides(t, n: int, what: str, least=None):
@@ -609,75 +608,50 @@ def _view_strides(t, n: int, what: str, least=None):
     return strides
 
 
-# The calls below are a decode step's small kernels, a few microseconds each: their checks read
-# every tensor's type, device (get_device is -1 on the host), shape and strides once and leave the
-# wording of a refusal to _refuse.
-def _refuse(t, what, dtype, dev, shape):
+# The calls below are a decode step's small kernels, a few microseconds each: _step (csrc/step_bind.cpp,
+# built beside the library) checks their tensors and calls the library.
+_STEP = None
+
+
+def _load_step():
+    """The _step module, its calls bound to the loaded library."""
+    global _STEP, _current_device, _current_stream
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
-        got = f"{t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
-        raise TypeError(f"{what} must be a {dtype} device (cuda/hip) tensor, got {got}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what} is on {t.device}, other tensors on device {dev}")
-    raise ValueError(f"{what} must be {shape}, got {list(t.shape)} with strides {list(t.stride())}")
+    lib = load()
+    path = os.path.join(_HERE, "_step.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built: run `python -m gemv_prefill_decode_amd.build` "
+                           "(or __graft_entry__.build())")
+    from . import _step
+    _step.bind(*(ctypes.cast(getattr(lib, "qmm_" + n), ctypes.c_void_p).value
+                 for n in ("paged_extend", "kv_append", "paged_attention", "paged_attention_workspace_bytes",
+                           "add_rmsnorm", "add_rmsnorm_q8")))
+    _current_device = getattr(torch._C, "_cuda_getDevice", None)
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _STEP = _step
+    return _step
 
 
-def _packed(torch, t, what, dtype, dev, shape):
-    """Pointer of a contiguous tensor of this shape."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    return _refuse(t, what, dtype, dev, f"contiguous {list(shape)}")
-
-
-def _f32_rows(torch, t, what, dev, n, row, heads=0):
-    """(pointer, row stride) of a float32 tensor [n, row], or [n, heads, row / heads] with its heads
-    side by side; rows any stride apart."""
-    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == dev:
-        shape = t.shape
-        if shape == (n, row) or (heads and shape == (n, heads, row // heads)):
-            if t.is_contiguous():
-                return t.data_ptr(), row
-            stride = t.stride()
-            if stride[-1] == 1 and (len(shape) == 2 or heads == 1 or stride[1] == row // heads):
-                return t.data_ptr(), (stride[0] if n > 1 else row)
-    return _refuse(t, what, torch.float32, dev,
-                   f"[{n}, {row}]" + (f" or [{n}, {heads}, {row // heads}]" if heads else "") + " with contiguous rows")
-
-
-def _table(torch, t, dev, batch):
-    """(pointer, entries per row, row stride) of a block table."""
-    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and t.dim() == 2:
-        n, width = t.shape
-        ld, unit = t.stride()
-        if n == batch and (unit == 1 or width == 1):
-            return t.data_ptr(), width, (ld if n > 1 else width)
-    return _refuse(t, "block_table", torch.int32, dev, f"[{batch}, max_pages] with contiguous rows")
-
-
-def _call(torch, dev, f, args, stream):
-    """A library call on device dev, on the given stream or the device's current one."""
-    if torch._C._cuda_getDevice() == dev:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+def _run(f, dev, stream, *args):
+    """f on device dev, on the given stream or the device's current one."""
+    if stream is None and _current_device() == dev:
+        st = f(_current_stream(dev), dev, *args)
     else:
+        import torch
         with torch.cuda.device(dev):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+            st = f(_current_stream(dev) if stream is None else stream.cuda_stream, dev, *args)
     if st != 0:
-        raise QmmError(st, f.__name__)
+        raise QmmError(st, "qmm_" + f.__name__)
 
 
-def _new(torch, shape, dtype, like, stream):
+def _new(shape, dtype, like, stream):
     """An output (or workspace) on like's device, allocated on the stream that writes it: memory of
     another stream may still be read there."""
+    import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _device_of(torch, t, what):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{what} must be a device (cuda/hip) tensor")
-    return t.get_device()
 
 
 def paged_extend(block_table, cached_lens, new_lens, free_pages, page_size: int, n_rows: int, seq_lens=None,
@@ -688,29 +662,18 @@ def paged_extend(block_table, cached_lens, new_lens, free_pages, page_size: int,
     pages_used [1]), all int32.  slots and positions are those of the new tokens' rows, sequence
     after sequence, -1 behind the last row and (slots) for a sequence that is refused because its
     table row or the free list is too short: its seq_lens entry stays cached_lens."""
-    import torch
-    lib = _LIB or load()
-    dev = _device_of(torch, block_table, "block_table")
-    i32 = torch.int32
-    batch = cached_lens.shape[0]
-    n_free = free_pages.numel()
-    table, max_pages, ld = _table(torch, block_table, dev, batch)
+    step = _STEP or _load_step()
+    dev = step.device(block_table, "block_table")
     if seq_lens is None:
-        seq_lens = _new(torch, batch, i32, block_table, stream)
+        seq_lens = _new(cached_lens.shape, cached_lens.dtype, block_table, stream)
     if slots is None:
-        slots = _new(torch, n_rows, i32, block_table, stream)
+        slots = _new(n_rows, cached_lens.dtype, block_table, stream)
     if positions is None:
-        positions = _new(torch, n_rows, i32, block_table, stream)
+        positions = _new(n_rows, cached_lens.dtype, block_table, stream)
     if pages_used is None:
-        pages_used = _new(torch, 1, i32, block_table, stream)
-    one, rows = (batch,), (n_rows,)
-    args = (table, ld, _packed(torch, seq_lens, "seq_lens", i32, dev, one),
-            _packed(torch, slots, "slots", i32, dev, rows), _packed(torch, positions, "positions", i32, dev, rows),
-            _packed(torch, pages_used, "pages_used", i32, dev, (1,)),
-            _packed(torch, cached_lens, "cached_lens", i32, dev, one),
-            _packed(torch, new_lens, "new_lens", i32, dev, one),
-            _packed(torch, free_pages, "free_pages", i32, dev, (n_free,)), batch, max_pages, page_size, n_free, n_rows)
-    _call(torch, dev, lib.qmm_paged_extend, args, stream)
+        pages_used = _new(1, cached_lens.dtype, block_table, stream)
+    _run(step.paged_extend, dev, stream, block_table, cached_lens, new_lens, free_pages, page_size, n_rows, seq_lens,
+         slots, positions, pages_used)
     return seq_lens, slots, positions, pages_used
 
 
@@ -718,13 +681,8 @@ def kv_append(cache: KVCache, k, v, slots, stream=None):
     """Writes new keys and values (float32 [n, n_kv, head_dim], or [n, n_kv*head_dim]; rows any
     stride apart, as views of a fused projection's output) into their slots (int32 [n]; a slot
     outside the cache, such as -1, is skipped; the others must differ)."""
-    import torch
-    lib = _LIB or load()
-    dev, row, heads = cache._index, cache._row, cache.n_kv
-    n = slots.shape[0]
-    args = (cache._ptr, *_f32_rows(torch, k, "k", dev, n, row, heads), *_f32_rows(torch, v, "v", dev, n, row, heads),
-            _packed(torch, slots, "slots", torch.int32, dev, (n,)), n)
-    _call(torch, dev, lib.qmm_kv_append, args, stream)
+    step = _STEP or _load_step()
+    _run(step.kv_append, cache._index, stream, cache._ptr, k, v, slots)
 
 
 def paged_attention_workspace_bytes(batch: int, n_q: int, cache: KVCache, max_pages: int) -> int:
@@ -745,40 +703,22 @@ def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=No
     a padded row (its output is zero).  scale: 1/sqrt(head_dim) by default.  lse: a float32
     [batch, n_q] tensor that takes the log-sum-exp of the scores.  workspace: "auto" (allocated
     for the call, from the graph's own memory under capture) or a device tensor of at least
-    paged_attention_workspace_bytes() bytes that no other call uses at the same time."""
-    import torch
-    lib = _LIB or load()
-    dev, d = cache._index, cache.head_dim
-    batch = seq_lens.shape[0]
-    n_q = q.shape[1] if q.dim() == 3 else q.shape[-1] // d
-    row = n_q * d
-    qp, ldq = _f32_rows(torch, q, "q", dev, batch, row, n_q)
+    paged_attention_workspace_bytes() bytes that no other call uses at the same time.  A caller
+    that knows a bound on the lengths may pass fewer columns of a wider block_table: up to 512
+    tokens per row take one kernel and no workspace."""
+    step = _STEP or _load_step()
     if out is None:
-        out = _new(torch, q.shape, torch.float32, q, stream)
-    op, ldo = _f32_rows(torch, out, "out", dev, batch, row, n_q)
-    table, max_pages, ld = _table(torch, block_table, dev, batch)
-    lp = None if lse is None else _packed(torch, lse, "lse", torch.float32, dev, (batch, n_q))
-    lens = _packed(torch, seq_lens, "seq_lens", torch.int32, dev, (batch,))
-    ws, ws_len = None, 0
-    if workspace is not None:
-        if isinstance(workspace, str):
-            if workspace != "auto":
-                raise ValueError("workspace must be 'auto', None or a tensor")
-            if torch._C._cuda_getDevice() == dev:
-                ws_len = lib.qmm_paged_attention_workspace_bytes(batch, n_q, cache.n_kv, d, max_pages, cache.page_size)
-            else:
-                ws_len = paged_attention_workspace_bytes(batch, n_q, cache, max_pages)
-            if ws_len > 0:
-                workspace = _new(torch, ws_len, torch.uint8, q, stream)
-                ws = workspace.data_ptr()
-            else:
-                ws_len = 0
-        else:
-            ws_len = workspace.numel() * workspace.element_size()
-            ws = _packed(torch, workspace, "workspace", workspace.dtype, dev, workspace.shape)
-    args = (op, ldo, lp, qp, ldq, cache._ptr, table, ld, lens, batch, n_q, max_pages,
-            d ** -0.5 if scale is None else scale, ws, ws_len)
-    _call(torch, dev, lib.qmm_paged_attention, args, stream)
+        out = _new(q.shape, q.dtype, q, stream)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto', None or a tensor")
+        workspace = True
+        if stream is not None:
+            import torch
+            n = paged_attention_workspace_bytes(seq_lens.shape[0], q[0].numel() // cache.head_dim, cache,
+                                                block_table.shape[1])
+            workspace = _new(n, torch.uint8, q, stream) if n > 0 else None
+    _run(step.paged_attention, cache._index, stream, cache._ptr, q, block_table, seq_lens, scale, out, lse, workspace)
     return out
 
 
@@ -786,39 +726,26 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-5, y=None, h=None, str
     """Residual addition and RMS norm; returns (y, h): h = x + residual (None without a residual,
     unless a tensor is given for it) and y = h * weight / sqrt(mean(h*h) + eps), float32 [n, k],
     k a multiple of 4.  Rows of any of them may be any multiple of 4 apart."""
-    import torch
-    lib = _LIB or load()
-    dev = _device_of(torch, x, "x")
-    n, k = x.shape
+    step = _STEP or _load_step()
+    dev = step.device(x, "x")
     if y is None:
-        y = _new(torch, (n, k), torch.float32, x, stream)
+        y = _new(x.shape, x.dtype, x, stream)
     if h is None and residual is not None:
-        h = _new(torch, (n, k), torch.float32, x, stream)
-    args = (*_f32_rows(torch, y, "y", dev, n, k), *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)),
-            *_f32_rows(torch, x, "x", dev, n, k),
-            *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
-            _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps)
-    _call(torch, dev, lib.qmm_add_rmsnorm, args, stream)
+        h = _new(x.shape, x.dtype, x, stream)
+    _run(step.add_rmsnorm, dev, stream, x, weight, residual, eps, y, h)
     return y, h
 
 
 def add_rmsnorm_q8(x, weight, residual=None, eps: float = 1e-5, q=None, d=None, h=None, stream=None):
     """add_rmsnorm with y as Q8_1 activations; returns (q int8 [n, k], d float32 [n, k/32], h), q
     and d as moe_gateup_q8 takes them.  k a multiple of 32."""
-    import torch
-    lib = _LIB or load()
-    dev = _device_of(torch, x, "x")
-    n, k = x.shape
-    if q is None:
-        q = _new(torch, (n, k), torch.int8, x, stream)
-    if d is None:
-        d = _new(torch, (n, k // 32), torch.float32, x, stream)
+    step = _STEP or _load_step()
+    dev = step.device(x, "x")
+    if q is None or d is None:
+        import torch
+        q = _new(x.shape, torch.int8, x, stream) if q is None else q
+        d = _new((x.shape[0], x.shape[1] // 32), torch.float32, x, stream) if d is None else d
     if h is None and residual is not None:
-        h = _new(torch, (n, k), torch.float32, x, stream)
-    args = (_packed(torch, q, "q", torch.int8, dev, (n, k)),
-            _packed(torch, d, "d", torch.float32, dev, (n, k // 32)),
-            *((None, 0) if h is None else _f32_rows(torch, h, "h", dev, n, k)), *_f32_rows(torch, x, "x", dev, n, k),
-            *((None, 0) if residual is None else _f32_rows(torch, residual, "residual", dev, n, k)),
-            _packed(torch, weight, "weight", torch.float32, dev, (k,)), n, k, eps)
-    _call(torch, dev, lib.qmm_add_rmsnorm_q8, args, stream)
+        h = _new(x.shape, x.dtype, x, stream)
+    _run(step.add_rmsnorm_q8, dev, stream, x, weight, residual, eps, q, d, h)
     return q, d, h

@@ -3,7 +3,8 @@
     python -m gemv_prefill_decode_amd.build        # or __graft_entry__.build()
 
 Each translation unit is compiled with hipcc in parallel, then linked into
-gemv_prefill_decode_amd/libqmm.so.  Packed-f32 VALU instructions are disabled
+gemv_prefill_decode_amd/libqmm.so; _step.so beside it is the Python module of
+the decode step's calls.  Packed-f32 VALU instructions are disabled
 (-packed-fp32-ops) for all device code.
 """
 
@@ -20,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libqmm.so")
+STEP_OUT = os.path.join(PKG, "_step.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["gemv.hip", "moe.hip", "gemm_mfma.hip", "gemm_lds.hip", "noalloc.hip", "kv_cache.hip", "attention.hip",
@@ -32,6 +34,10 @@ def hipcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm)")
+
+
+def rocm_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
 
 
 def _flags():
@@ -75,9 +81,31 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, OUT)
+    build_step()
     if verbose:
         print(f"built {OUT}")
     return OUT
+
+
+def build_step() -> str:
+    """The Python module of the decode step's calls (checks torch tensors and
+    calls the library through addresses it is given): host code only."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(rocm_home(), "include")]
+    tmp = STEP_OUT + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    cmd += [x for i in inc for x in ("-isystem", i)]
+    cmd += [os.path.join(CSRC, "step_bind.cpp"), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for step_bind.cpp:\n" + r.stdout + r.stderr)
+    os.replace(tmp, STEP_OUT)
+    return STEP_OUT
 
 
 # ---------------------------------------------------------------- sanitized host build
