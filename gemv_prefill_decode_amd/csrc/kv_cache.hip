@@ -15,86 +15,93 @@ namespace {
 // without communication between work groups: each scans all sequences in
 // passes of THREADS (two sums), and writes its own range of rows and its
 // stride of new table entries, which it finds in the pass by bisection.
-// Measured: 64 sequences of one new token 3.7 us (1024 threads instead of 256:
-// 6.1); 512 prompts with 88600 rows 7.0 us (4096 rows per work group instead of
-// 1024: 10.4).
-template <int THREADS, typename T>
-__device__ __forceinline__ T block_inclusive(T v, T* waves, T* total) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const T u = __shfl_up(v, s);
-        if (lane >= s) v += u;
-    }
-    if (lane == 63) waves[w] = v;
-    __syncthreads();
-    T t = 0;
-    for (int i = 0; i < THREADS / 64; ++i) {
-        if (i < w) v += waves[i];
-        t += waves[i];
-    }
-    *total = t;
+// Measured: 64 sequences of one new token 3.2 us, 512 prompts with 88600 rows
+// 3.9, 1024 prompts on pages of one token 5.2 (with 64-bit sums, LDS shuffles
+// and a branching bisection 4.0, 7.0 and 13.0; a launch alone 1.6).
+//
+// Sums of rows saturate at 2^32 - 1, far behind any row that is written
+// (saturating addition is associative, so the scan may take it in any order).
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// Inclusive sums over the wave's lanes: row shifts within 16 lanes, then the
+// rows' last lanes handed on.
+template <bool SAT>
+__device__ __forceinline__ uint32_t wave_inclusive(uint32_t v) {
+    auto add = [](uint32_t a, uint32_t b) { return SAT ? add_sat(a, b) : a + b; };
+    v = add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, true));   // row_shr:1
+    v = add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, true));   // row_shr:2
+    v = add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, true));   // row_shr:4
+    v = add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, true));   // row_shr:8
+    v = add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));  // row_bcast:15
+    v = add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));  // row_bcast:31
     return v;
 }
 
 // First index whose inclusive sum exceeds x (sums do not decrease).
-template <int THREADS, typename T>
-__device__ __forceinline__ int bisect(const T* sums, T x) {
-    int lo = 0, hi = THREADS - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] > x)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
+template <int THREADS>
+__device__ __forceinline__ int bisect(const uint32_t* sums, uint32_t x) {
+    int lo = 0;
+#pragma unroll
+    for (int step = THREADS / 2; step > 0; step >>= 1)
+        if (sums[lo + step - 1] <= x) lo += step;
     return lo;
 }
 
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void paged_extend_kernel(const ExtendArgs a, int rows_per_group) {
-    __shared__ int64_t row_end[THREADS], row_waves[THREADS / 64];
-    __shared__ int need_end[THREADS], need_waves[THREADS / 64];
-    __shared__ int cached[THREADS], fresh[THREADS];
+    constexpr int WAVES = THREADS / 64;
+    __shared__ uint32_t row_end[THREADS], need_end[THREADS];
+    __shared__ uint32_t row_waves[WAVES], need_waves[WAVES];
+    __shared__ int cached[THREADS];
     __shared__ bool taken[THREADS];
-    const int tid = threadIdx.x;
-    const int64_t lo = (int64_t)blockIdx.x * rows_per_group;
-    const int64_t hi = lo + rows_per_group < a.n_rows ? lo + rows_per_group : a.n_rows;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t lo = blockIdx.x * (uint32_t)rows_per_group, n_rows = (uint32_t)a.n_rows;
+    const uint32_t hi = lo + rows_per_group < n_rows ? lo + rows_per_group : n_rows;
     const int mask = (1 << a.page_log2) - 1;
     auto pages = [&](int64_t tokens) { return (int)((tokens + mask) >> a.page_log2); };
-    int64_t rows_before = 0;
-    int need_before = 0;
+    uint32_t rows_before = 0, need_before = 0;
     for (int base = 0, pass = 0; base < a.batch; base += THREADS, ++pass) {
         const int b = base + tid;
         const int c = b < a.batch ? a.cached[b] : 0, n = b < a.batch ? a.fresh[b] : 0;
         bool ok = c >= 0 && n >= 0 && (int64_t)c + n <= a.capacity;
         const int need = ok ? pages((int64_t)c + n) - pages(c) : 0;
-        int64_t rows_total;
-        int need_total;
-        const int64_t rows_incl = rows_before + block_inclusive<THREADS, int64_t>(n > 0 ? n : 0, row_waves, &rows_total);
-        const int need_incl = need_before + block_inclusive<THREADS, int>(need, need_waves, &need_total);
-        ok = ok && (need == 0 || need_incl <= a.n_free);
-        row_end[tid] = rows_incl;
-        need_end[tid] = need_incl;
+        uint32_t rows = wave_inclusive<true>(n > 0 ? (uint32_t)n : 0u), needs = wave_inclusive<false>((uint32_t)need);
+        if (lane == 63) {
+            row_waves[w] = rows;
+            need_waves[w] = needs;
+        }
         cached[tid] = c;
-        fresh[tid] = n > 0 ? n : 0;
+        __syncthreads();
+        // the waves before this one, and the whole pass
+        const uint32_t rw = wave_inclusive<true>(lane < WAVES ? row_waves[lane] : 0u);
+        const uint32_t nw = wave_inclusive<false>(lane < WAVES ? need_waves[lane] : 0u);
+        if (w > 0) {
+            rows = add_sat(rows, __builtin_amdgcn_readlane(rw, w - 1));
+            needs += __builtin_amdgcn_readlane(nw, w - 1);
+        }
+        rows = add_sat(rows, rows_before);
+        needs += need_before;
+        const uint32_t rows_after = add_sat(rows_before, __builtin_amdgcn_readlane(rw, 63));
+        const uint32_t need_after = need_before + __builtin_amdgcn_readlane(nw, 63);
+        ok = ok && (need == 0 || needs <= (uint32_t)a.n_free);
+        row_end[tid] = rows;
+        need_end[tid] = needs;
         taken[tid] = ok;
         if (b < a.batch && pass % gridDim.x == blockIdx.x) a.seq_lens[b] = ok ? c + n : c;
         __syncthreads();
 
         // new table entries
-        for (int e = need_before + blockIdx.x * THREADS + tid; e < need_before + need_total && e < a.n_free;
+        for (uint32_t e = need_before + blockIdx.x * THREADS + tid; e < need_after && e < (uint32_t)a.n_free;
              e += gridDim.x * THREADS) {
-            const int s = bisect<THREADS>(need_end, e);
-            const int begin = s ? need_end[s - 1] : need_before;
-            if (taken[s]) a.table[(int64_t)(base + s) * a.table_stride + pages(cached[s]) + (e - begin)] = a.free_pages[e];
+            const int page = a.free_pages[e], s = bisect<THREADS>(need_end, e);
+            const uint32_t begin = s ? need_end[s - 1] : need_before;
+            if (taken[s]) a.table[(int64_t)(base + s) * a.table_stride + pages(cached[s]) + (e - begin)] = page;
         }
         // this work group's rows that belong to the pass
-        const int64_t r_lo = lo > rows_before ? lo : rows_before;
-        const int64_t r_hi = hi < rows_before + rows_total ? hi : rows_before + rows_total;
-        for (int64_t r = r_lo + tid; r < r_hi; r += THREADS) {
+        const uint32_t r_lo = lo > rows_before ? lo : rows_before, r_hi = hi < rows_after ? hi : rows_after;
+        for (uint32_t r = r_lo + tid; r < r_hi; r += THREADS) {
             const int s = bisect<THREADS>(row_end, r);
-            const int pos = (int)(cached[s] + (r - (row_end[s] - fresh[s])));
+            const int pos = (int)((int64_t)cached[s] + (r - (s ? row_end[s - 1] : rows_before)));
             int slot = -1;
             if (taken[s]) {
                 const int col = pos >> a.page_log2, have = pages(cached[s]);
@@ -106,15 +113,15 @@ __global__ __launch_bounds__(THREADS) void paged_extend_kernel(const ExtendArgs 
             a.slots[r] = slot;
             a.positions[r] = pos;
         }
-        rows_before += rows_total;
-        need_before += need_total;
-        __syncthreads();
+        rows_before = rows_after;
+        need_before = need_after;
+        if (base + THREADS < a.batch) __syncthreads();
     }
-    for (int64_t r = (lo > rows_before ? lo : rows_before) + tid; r < hi; r += THREADS) {
+    for (uint32_t r = (lo > rows_before ? lo : rows_before) + tid; r < hi; r += THREADS) {
         a.slots[r] = -1;
         a.positions[r] = -1;
     }
-    if (blockIdx.x == 0 && tid == 0) *a.pages_used = need_before;
+    if (blockIdx.x == 0 && tid == 0) *a.pages_used = (int)need_before;
 }
 
 // ------------------------------------------------------------------ append
