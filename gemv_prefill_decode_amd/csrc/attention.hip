@@ -788,7 +788,6 @@ void launch(const AttnArgs& a, hipStream_t st) {
         paged_attn_join_kernel<32 * NB><<<dim3((unsigned)(a.meta_by_unit ? units : a.groups)), 256, 0, st>>>(a);
 }
 
-
 template <int KIND>
 void launch_kind(const AttnArgs& a, int head_dim, hipStream_t st) {
     switch (head_dim / 32) {

@@ -357,6 +357,7 @@ int check_cache(const qmm_kv_cache* c, KvExtent* e) {
         if (s % unit != 0) return QMM_ERR_ALIGN;
     }
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QMM_ERR_ALIGN;
+    if (c->k == c->v) return QMM_ERR_ALIAS;
     int64_t tokens;
     if (!mul_ok(c->n_pages, c->page_size, &tokens) || tokens > KV_TOKENS_MAX || c->n_kv > 65535) return QMM_ERR_RANGE;
     const int64_t elems = strided_extent(c, c->page_stride, c->head_stride, c->slot_stride, c->head_dim);

@@ -35,7 +35,7 @@ BAD_CACHES = [
     (SHAPE, dict(head_dim=0)), (K_ALIGN, dict(head_dim=48)), (RANGE, dict(head_dim=288)),
     (SHAPE, dict(slot_stride=32)), (SHAPE, dict(head_stride=0)), (SHAPE, dict(page_stride=-64)),
     (ALIGN, dict(slot_stride=68)), (ALIGN, dict(kind=2, slot_stride=72)), (ALIGN, dict(k=P[0].value + 8)),
-    (RANGE, dict(n_pages=1 << 27)), (RANGE, dict(n_kv=65536)),
+    (ALIAS, dict(v=P[0].value)), (RANGE, dict(n_pages=1 << 27)), (RANGE, dict(n_kv=65536)),
     (RANGE, dict(n_pages=1 << 20, page_stride=1 << 20)),          # 2 TiB between the first and the last page
     (RANGE, dict(page_stride=1 << 60)), (SHAPE, dict(kind=2, scale_slot_stride=0)),
     (ALIGN, dict(kind=2, v_scale=P[3].value + 2)),
