@@ -496,6 +496,36 @@ def test_attention_is_deterministic_on_any_stream_and_under_capture():
     assert torch.equal(want, outs[0])
 
 
+def test_calls_at_the_same_time_on_two_streams():
+    """Steps of two caches on two streams, each with append, page tables, attention and norm: neither
+    disturbs the other (own workspaces), and both equal their serial results."""
+    torch, qmm = _torch(), _qmm()
+    cases = [_case(k, [2500, 40, 0, 900], 4, 2, 64, 16, seed=s, tokens=4000) for s, k in ((3, "f16"), (4, "q8"))]
+    w = torch.ones(512, device="cuda")
+
+    def one(c, stream=None):
+        table, lens = c["dev"]
+        out = qmm.paged_attention(c["q"], c["cache"], table, lens, stream=stream)
+        y, _ = qmm.add_rmsnorm(out.flatten(1), w, stream=stream)
+        _, slots, pos, _ = qmm.paged_extend(c["tab2"], lens, c["new"], c["free"], 16, 8, stream=stream)
+        return out, y, slots, pos
+
+    for c in cases:
+        c["dev"] = (torch.from_numpy(c["table"]).cuda(), torch.tensor(c["lens"], dtype=torch.int32, device="cuda"))
+        c["tab2"], c["new"] = c["dev"][0].clone(), torch.tensor([1, 2, 3, 1], dtype=torch.int32, device="cuda")
+        c["free"] = torch.arange(8, dtype=torch.int32, device="cuda")
+        c["want"] = [t.clone() for t in one(c)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        got = [one(c, s) for c, s in zip(cases, streams)]
+        for s in streams:
+            s.synchronize()
+        for c, g in zip(cases, got):
+            for x, y in zip(g, c["want"]):
+                assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------------ norm
 NORM_SHAPES = [(1, 4), (1, 32), (3, 36), (7, 64), (5, 100), (9, 128), (4, 256), (33, 260), (2, 1024), (5, 1028), (3, 2048),
                (16, 4096), (2, 4608), (3, 8192), (2, 12000), (1, 16384), (2, 16388), (2, 40000), (1000, 32), (257, 512)]
