@@ -827,17 +827,20 @@ AttnPlan plan_paged_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t 
     const int64_t most = (batch * tiles + 3) / 4;
     const int64_t want = (int64_t)num_cu * 2;
     // Short tables: a work group per unit saves the scan of the lengths and the
-    // join (8 kv heads of 128, 4 query heads each, f16, one sequence: 32 tokens
-    // 4.1 us against 6.7, 256 tokens 7.3 / 9.1, 512 tokens 10.8 / 10.4, 1024
-    // tokens 16.3 / 9.9; 64 sequences of 512 27.7 / 30.6), as long as the units
-    // are not many more than fit the device at a time (256 sequences of 32:
-    // 18.4 us against 14.9).
-    p.per_unit = tiles <= 16 && batch * p.head_spaces <= 4 * (int64_t)num_cu;
+    // join, up to a length at which its waves' own tiles take longer, which few
+    // units reach sooner than many (8 kv heads of 128, f16, this way against
+    // the split: one sequence of 256 tokens 6.9 and 9.1 us, 384 8.9 / 9.6, 512
+    // 10.6 / 9.6; 32 sequences of 512 14.6 / 18.7).  Longer, only even lengths
+    // gain (32 sequences of 1024 24.7 / 28.4, one of 1024 and 31 of 64 16.7 /
+    // 12.2).  Not where the units are many more than fit the device at a time
+    // (256 sequences of 64: 22.9 / 18.5).
+    const int64_t units = batch * p.head_spaces;
+    p.per_unit = tiles <= (2 * units >= num_cu ? 16 : 12) && units <= 4 * (int64_t)num_cu;
     int64_t cuts = want / p.head_spaces;
     if (cuts > most) cuts = most;
     p.cuts = cuts < 1 ? 1 : (int)cuts;
     p.groups = (int)(p.cuts * p.head_spaces);
-    p.meta_by_unit = batch * p.head_spaces <= p.groups;
+    p.meta_by_unit = units <= p.groups;
     p.meta_bytes = ((int64_t)p.groups * 8 + 255) / 256 * 256;
     const int64_t part = (int64_t)part_floats(p.heads_per_block, (int)head_dim) * 4;
     p.ws_bytes = !p.per_unit ? p.meta_bytes + (2 * p.groups * part + 255) / 256 * 256 : 0;

@@ -560,8 +560,8 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * <= 2^30, batch*n_q and batch*(ceil(max_pages*page_size/32) + 2) below 2^31.
  * The launch depends on the sizes alone, never on the lengths: a caller that
  * knows a bound on the lengths may pass fewer columns of a wider table
- * (max_pages below table_stride); up to 512 tokens per row one kernel does
- * the whole.  Up to 16 query heads per kv head share one pass over a row;
+ * (max_pages below table_stride): with up to 384 tokens per row (512 where
+ * sequences and heads are many) one kernel does the whole, without a workspace.  Up to 16 query heads per kv head share one pass over a row;
  * n_q/n_kv above that takes one pass per 16.
  */
 int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int64_t ldq, const qmm_kv_cache* cache,
