@@ -705,7 +705,7 @@ def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=No
     for the call, from the graph's own memory under capture) or a device tensor of at least
     paged_attention_workspace_bytes() bytes that no other call uses at the same time.  A caller
     that knows a bound on the lengths may pass fewer columns of a wider block_table: up to 384
-    tokens per row take one kernel and no workspace."""
+    tokens per row mostly take one kernel and no workspace."""
     step = _STEP or _load_step()
     if out is None:
         out = _new(q.shape, q.dtype, q, stream)

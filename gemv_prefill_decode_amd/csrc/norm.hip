@@ -119,23 +119,37 @@ __global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(const NormArgs a) 
 }
 
 template <int THREADS, int T, int V, bool LOOP = false>
-void launch(const NormArgs& a, hipStream_t st) {
+void launch(const NormArgs& all, hipStream_t st) {
     constexpr int ROWS = THREADS / T;
-    const dim3 grid((unsigned)((a.n + ROWS - 1) / ROWS));
     // Large inputs are read past the caches: from HBM 2048 x 4096 takes 23.1 us
     // (else 24.2), 2048 x 4608 26.0 (33.8), 512 x 14336 20.5 (27.5), 2048 x 4096
     // to Q8_1 23.5 (28.0).  Inputs that the 256 MB cache behind the L2s still
     // holds from their producer lose by it (2048 x 4096 26.3 against 23.7, 1000
     // x 4608 to Q8_1 15.5 against 14.8), so only those of over 48 MB.
-    const bool nt = !LOOP && a.n * a.k * (a.r ? 8 : 4) > ((int64_t)48 << 20);
-    if (a.q && nt)
-        add_rmsnorm_kernel<THREADS, T, V, true, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
-    else if (a.q)
-        add_rmsnorm_kernel<THREADS, T, V, true, false, LOOP><<<grid, THREADS, 0, st>>>(a);
-    else if (nt)
-        add_rmsnorm_kernel<THREADS, T, V, false, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
-    else
-        add_rmsnorm_kernel<THREADS, T, V, false, false, LOOP><<<grid, THREADS, 0, st>>>(a);
+    const bool nt = !LOOP && all.n * all.k * (all.r ? 8 : 4) > ((int64_t)48 << 20);
+    // a launch has fewer than 2^32 threads
+    constexpr int64_t MOST = ((int64_t)1 << 31) / THREADS * ROWS;
+    for (int64_t first = 0; first < all.n; first += MOST) {
+        NormArgs a = all;
+        a.n = all.n - first < MOST ? all.n - first : MOST;
+        a.x += first * a.x_stride;
+        if (a.r) a.r += first * a.r_stride;
+        if (a.h) a.h += first * a.h_stride;
+        if (a.y) a.y += first * a.y_stride;
+        if (a.q) {
+            a.q += first * a.k;
+            a.d += first * (a.k / 32);
+        }
+        const dim3 grid((unsigned)((a.n + ROWS - 1) / ROWS));
+        if (a.q && nt)
+            add_rmsnorm_kernel<THREADS, T, V, true, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
+        else if (a.q)
+            add_rmsnorm_kernel<THREADS, T, V, true, false, LOOP><<<grid, THREADS, 0, st>>>(a);
+        else if (nt)
+            add_rmsnorm_kernel<THREADS, T, V, false, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
+        else
+            add_rmsnorm_kernel<THREADS, T, V, false, false, LOOP><<<grid, THREADS, 0, st>>>(a);
+    }
 }
 
 }  // namespace

@@ -541,8 +541,9 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * outside [0, n_pages) among the pages that hold a sequence's tokens, give
  * NaN for that sequence's outputs.  Table entries behind the last page, and
  * cache rows behind the last token, are never used.  A non-finite query, key
- * or value makes the outputs that it enters non-finite; the same holds for
- * scores beyond the f32 range.
+ * or value makes the outputs that it enters non-finite, except that a score
+ * of -inf may count as a weight of zero; the same holds for scores beyond the
+ * f32 range.
  * f32 arithmetic: f32 operands enter the matrix cores as two f16 (three
  * bf16) parts, products and sums are f32; the exponential and logarithm are
  * the hardware's.
@@ -561,8 +562,10 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * The launch depends on the sizes alone, never on the lengths: a caller that
  * knows a bound on the lengths may pass fewer columns of a wider table
  * (max_pages below table_stride): with up to 384 tokens per row (512 where
- * sequences and heads are many) one kernel does the whole, without a workspace.  Up to 16 query heads per kv head share one pass over a row;
- * n_q/n_kv above that takes one pass per 16.
+ * sequences times kv heads are half the CUs or more) one kernel does the
+ * whole, without a workspace, unless they are more than four times the CUs.
+ * Up to 16 query heads per kv head share one pass over a row; n_q/n_kv above
+ * that takes one pass per 16.
  */
 int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int64_t ldq, const qmm_kv_cache* cache,
                         const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens, int64_t batch,

@@ -574,6 +574,24 @@ def test_norm_q8(n, k, residual):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("q8", [False, True])
+def test_norm_of_more_rows_than_a_launch_holds(q8):
+    """2^24 rows of a work group of 256 threads each pass a launch's 2^32 threads."""
+    torch, qmm = _torch(), _qmm()
+    n, k, step_rows = (1 << 24) + 3, 288, 1 << 22
+    if torch.cuda.mem_get_info()[0] < 50 << 30:
+        pytest.skip("needs 50 GB of free device memory")
+    gh.note(f"norm n={n} k={k} q8={q8}")
+    x, w = torch.randn(n, k, device="cuda"), torch.rand(k, device="cuda")
+    f = qmm.add_rmsnorm_q8 if q8 else qmm.add_rmsnorm
+    got = f(x, w)[:-1]
+    for at in range(0, n, step_rows):
+        for g, part in zip(got, f(x[at:at + step_rows], w)[:-1]):
+            assert torch.equal(g[at:at + step_rows], part)
+    del got, g, part, x
+    torch.cuda.empty_cache()
+
+
 def test_norm_refuses_what_it_cannot_take():
     torch, qmm = _torch(), _qmm()
     x, w = torch.zeros(2, 64, device="cuda"), torch.ones(64, device="cuda")
