@@ -414,10 +414,10 @@ struct Segment {
             l = l * alpha + sum;
             if constexpr (Q8) {
                 // value scales relative to the largest so far, rounded up to a power of two
-                float big = vs[0];
+                float big = fabsf(vs[0]);
 #pragma unroll
                 for (int j = 1; j < 8; ++j) big = fmaxf(big, fabsf(vs[j]));
-                big = max_c(fabsf(big));
+                big = max_c(big);
                 int e = (int)(ubits(big) >> 23) + 1;
                 e = e < 2 ? 2 : (e > 253 ? 253 : e);
                 const float v2 = fmaxf(vexp, fbits((uint32_t)e << 23));

@@ -1,0 +1,29 @@
+"""The decode-step operators on the GPU at the edges of what their header allows: signed and far
+apart scales, values near the type's range, NaN in appended rows, every norm kernel."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import gpu_helpers as gh
+from test_gpu_step import _case, _check, _torch
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ 8-bit scales
+@pytest.mark.parametrize("q_mul", [0.0, 1.0])
+@pytest.mark.parametrize("big", [-10.0, 10.0, -1e3])
+def test_attention_signed_value_scales(big, q_mul):
+    """One value scale that is the largest in magnitude, at every place of two tiles in turn (a
+    sequence each), among scales of one and minus one; key scales of both signs.  A q of zeros
+    gives every token the largest weight."""
+    gh.note(f"attention value scale {big} q*{q_mul}")
+    c = _case("q8", [70] * 64, 2, 3, 64, 16, q_mul=q_mul, stale=False)
+    sign = 1.0 - 2.0 * (_torch().arange(16, device="cuda") % 3 == 1)
+    c["cache"].k_scale.copy_(0.02 * sign.expand_as(c["cache"].k_scale))
+    c["cache"].v_scale.copy_(sign.expand_as(c["cache"].v_scale))
+    for i in range(64):
+        c["cache"].v_scale[int(c["table"][i][i // 16]), :, i % 16] = big
+    _check(c)
