@@ -71,6 +71,7 @@ constexpr int occupancy(int kind, int nb) { return nb <= (kind == KV_Q8 ? 6 : 5)
 constexpr int UNIT_START = 2, START_MIN = 6;
 constexpr float PBITS = 14.0f;
 constexpr float P_UNIT = 6.103515625e-05f;  // 2^-14
+constexpr int VEXP_MIN = 15;                // its inverse times 2^14 is a normal number
 constexpr float LN2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -198,7 +199,11 @@ struct Segment {
 
     f32x4 acc[2 * NB];
     float m, l;
-    float vexp;      // 8-bit values: acc holds sums divided by this power of two
+    // 8-bit values: the largest weight times value scale so far, against the
+    // present maximum, and the exponent field of a power of two above it, which
+    // acc's sums are relative to
+    float vtop;
+    int vexp;
 
     // Rows of whole lines are read once and past the caches (non-temporal: 131071
     // tokens of f16 heads of 128 94.9 -> 91.1 us); rows that share lines are not
@@ -287,7 +292,8 @@ struct Segment {
         const int lane = threadIdx.x & 63, c = lane >> 4, i = lane & 15;
         m = -INFINITY;
         l = 0.0f;
-        vexp = fbits(1u << 23);
+        vtop = 0.0f;
+        vexp = VEXP_MIN;
 #pragma unroll
         for (int o = 0; o < 2 * NB; ++o) acc[o] = f32x4{0, 0, 0, 0};
         if (len <= 0) {
@@ -408,25 +414,32 @@ struct Segment {
             float p[8], sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                p[j] = __builtin_amdgcn_exp2f(s[j] - base + PBITS);
+                p[j] = __builtin_amdgcn_exp2f(Q8 ? s[j] - base : s[j] - base + PBITS);
                 sum += p[j];
             }
             l = l * alpha + sum;
             if constexpr (Q8) {
-                // value scales relative to the largest so far, rounded up to a power of two
-                float big = fabsf(vs[0]);
-#pragma unroll
-                for (int j = 1; j < 8; ++j) big = fmaxf(big, fabsf(vs[j]));
-                big = max_c(big);
-                int e = (int)(ubits(big) >> 23) + 1;
-                e = e < 2 ? 2 : (e > 253 ? 253 : e);
-                const float v2 = fmaxf(vexp, fbits((uint32_t)e << 23));
-                alpha *= vexp * fbits((254u << 23) - ubits(v2));
-                vexp = v2;
-                const float inv = fbits((254u << 23) - ubits(v2));
+                // A value's scale multiplies its probability.  The products are taken relative to
+                // a power of two above the head's largest so far, as that has faded since: a far
+                // larger scale of a token that weighs nothing takes no bits from the others
+                // (relative to the largest scale alone, 1e12 beside a weight of e^-60 lost them all).
+                float big = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    p[j] *= vs[j] * inv;
+                    p[j] *= vs[j];
+                    big = fmaxf(big, fabsf(p[j]));
+                }
+                vtop = fmaxf(vtop * alpha, max_c(big));
+                int e = (int)(ubits(vtop) >> 23) + 1;
+                e = e < VEXP_MIN ? VEXP_MIN : (e > 254 ? 254 : e);
+                int step = 127 + vexp - e;
+                step = step < 0 ? 0 : (step > 254 ? 254 : step);
+                alpha *= fbits((uint32_t)step << 23);
+                vexp = e;
+                const float inv = fbits((uint32_t)(127 + 14 + 127 - e) << 23);  // to at most 2^14
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    p[j] *= inv;
                     // The product as one f32 value: the compiler otherwise rounds it to f16 for the
                     // high part straight from its factors (v_fma_mixlo_f16), which near a tie is not
                     // the f16 that the low part was taken against (2^-11 off, seen about once in 10^4).
@@ -451,7 +464,8 @@ struct Segment {
         l = sum_c(l);
         if constexpr (Q8) {
 #pragma unroll
-            for (int o = 0; o < 2 * NB; ++o) acc[o] *= vexp;
+            for (int o = 0; o < 2 * NB; ++o) acc[o] *= fbits((uint32_t)vexp << 23);
+            l *= 1.0f / P_UNIT;  // as the other kinds' weights
         }
     }
 

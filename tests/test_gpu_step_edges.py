@@ -27,3 +27,20 @@ def test_attention_signed_value_scales(big, q_mul):
     for i in range(64):
         c["cache"].v_scale[int(c["table"][i][i // 16]), :, i % 16] = big
     _check(c)
+
+
+@pytest.mark.parametrize("tokens", [0, 9000])
+@pytest.mark.parametrize("place", [0, 20, 64, 199])
+def test_attention_far_value_scale_of_a_negligible_token(place, tokens):
+    """A token of weight e^-60 whose value scale is 1e12 times the others': these decide the output
+    and keep all their bits."""
+    torch = _torch()
+    gh.note(f"attention far scale at {place}, table for {tokens}")
+    c = _case("q8", [200], 2, 1, 64, 16, stale=False, tokens=tokens)
+    page, at = int(c["table"][0][place // 16]), place % 16
+    for h in range(2):
+        q = c["q"][0, h]
+        c["cache"].k[page, h, at] = (-100 * torch.sign(q)).to(torch.int8)
+        c["cache"].k_scale[page, h, at] = 60.0 / (c["scale"] * 100 * float(q.abs().sum()))
+        c["cache"].v_scale[page, h, at] = 1e12 * float(c["cache"].v_scale[:, h].abs().max())
+    _check(c)
