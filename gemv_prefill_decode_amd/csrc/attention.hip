@@ -112,6 +112,15 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
     const int n = a.lens[b];
     return (n < 0 || n > a.capacity) ? -1 : n;
 }
+// One over what the weight of a head's largest score counts in its sums (m, l
+// and acc, in registers and in parts).  f16: 2^14, sums of values of at most
+// 65504 stay far inside f32.  8-bit elements are as large as their scales: 2^-b
+// for up to 2^b tokens, so that a sum of weights times values is no larger than
+// the largest value.
+__device__ __forceinline__ float one_weight(int kind, int len) {
+    if (kind != KV_Q8) return P_UNIT;
+    return fbits((uint32_t)(127 + (len > 1 ? 32 - __builtin_clz(len - 1) : 0)) << 23);
+}
 // A unit without tokens still takes one tile, whose wave writes its outputs.
 __device__ __forceinline__ int seq_tiles(int len) { return len <= TILE ? 1 : (len + TILE - 1) / TILE; }
 
@@ -388,10 +397,11 @@ struct Segment {
             float s[8], vs[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                s[j] = s4[j / 4][j % 4] * qs;
                 if constexpr (Q8) {
-                    s[j] *= from_lane(sc, tok_of(j));
+                    s[j] = s4[j / 4][j % 4] * (qs * from_lane(sc, tok_of(j)));  // the factors alone may leave f32
                     vs[j] = from_lane(sc, 32 + tok_of(j));
+                } else {
+                    s[j] = s4[j / 4][j % 4] * qs;
                 }
             }
             if (TILE * (tt + 1) > len) {
@@ -463,9 +473,10 @@ struct Segment {
         if (__any(bad)) l = NAN;
         l = sum_c(l);
         if constexpr (Q8) {
+            const float u = 1.0f / one_weight(KIND, len);
 #pragma unroll
-            for (int o = 0; o < 2 * NB; ++o) acc[o] *= fbits((uint32_t)vexp << 23);
-            l *= 1.0f / P_UNIT;  // as the other kinds' weights
+            for (int o = 0; o < 2 * NB; ++o) acc[o] = acc[o] * (P_UNIT * u) * fbits((uint32_t)vexp << 23);
+            l *= u;
         }
     }
 
@@ -491,7 +502,10 @@ struct Segment {
     }
 };
 
-__device__ __forceinline__ float lse_of(float m, float l) { return (m + __builtin_amdgcn_logf(l * P_UNIT)) * LN2; }
+// unit: one_weight of the sequence
+__device__ __forceinline__ float lse_of(float m, float l, float unit) {
+    return (m + __builtin_amdgcn_logf(l * unit)) * LN2;
+}
 
 // A unit: (kv head, block of at most HEADS of its query heads, sequence).
 struct Unit {
@@ -616,7 +630,7 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
                 float* o = a.out + (int64_t)b * a.out_stride + (int64_t)(u.head0 + i) * D;
                 seg.each(inv, [&](int d, auto v) { *(decltype(v)*)(o + d) = v; });
                 if (a.lse && lane < 16)
-                    a.lse[(int64_t)b * a.n_q + u.head0 + i] = len == 0 ? -INFINITY : lse_of(seg.m, seg.l);
+                    a.lse[(int64_t)b * a.n_q + u.head0 + i] = len == 0 ? -INFINITY : lse_of(seg.m, seg.l, one_weight(KIND, len));
             }
         } else {
             const int slot = t == 0 ? 1 : 0;  // the unit starts in this wave, or came in from the one before
@@ -674,7 +688,7 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
             }
             if (whole) {
                 *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * D + d) = o * (1.0f / l);
-                if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l);
+                if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l, one_weight(KIND, seq_len(a, u.b)));
             } else {
                 *(f32x4*)(ws + row * D + d) = o;
                 if (d == 0) *(f32x2*)(ws + a.heads_per_block * D + 2 * row) = f32x2{top, l};
@@ -690,7 +704,8 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
 // starts at most one such unit): {work group or unit, following work groups}.
 struct Split {
     Unit u;
-    int g, n;  // first work group, parts
+    int g, n;    // first work group, parts
+    float unit;  // one_weight of its parts
 };
 __device__ __forceinline__ Split split_of(const AttnArgs& a) {
     const int2 info = a.meta[blockIdx.x];
@@ -698,7 +713,10 @@ __device__ __forceinline__ Split split_of(const AttnArgs& a) {
     Split s;
     s.g = a.meta_by_unit ? info.x : blockIdx.x;
     s.n = info.y == 0 ? 0 : info.y + 1;
-    if (s.n) s.u = unit_of(a, unit / a.batch, unit % a.batch);
+    if (s.n) {
+        s.u = unit_of(a, unit / a.batch, unit % a.batch);
+        s.unit = one_weight(a.kind, a.kind == KV_Q8 ? seq_len(a, s.u.b) : 1);
+    }
     return s;
 }
 
@@ -730,9 +748,10 @@ struct Sum {
                 if (p0 + j * step < s.n) add(v[j], ml[j].x, ml[j].y);
         }
     }
-    __device__ __forceinline__ void write(const AttnArgs& a, const Unit& u, int dim, int row, int d) const {
+    __device__ __forceinline__ void write(const AttnArgs& a, const Split& s, int dim, int row, int d) const {
+        const Unit& u = s.u;
         *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * dim + d) = o * (1.0f / l);
-        if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(m, l);
+        if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(m, l, s.unit);
     }
 };
 
@@ -765,7 +784,7 @@ __global__ __launch_bounds__(256) void paged_attn_join_wide_kernel(const AttnArg
     if (threadIdx.x >= 8) return;
 #pragma unroll
     for (int i = 1; i < 4; ++i) x.add(so[i][lane], sml[i].x, sml[i].y);
-    x.write(a, s.u, D, row, d);
+    x.write(a, s, D, row, d);
 }
 
 // Many units: one work group each (its start alone costs 0.5 ns of the whole
@@ -795,7 +814,7 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(const AttnArgs a) 
                 for (int p = 1; p < groups; ++p) x.add(so[p * span + tid], sml[p * span + tid].x, sml[p * span + tid].y);
             __syncthreads();
         }
-        if (pg == 0) x.write(a, s.u, D, row, d);
+        if (pg == 0) x.write(a, s, D, row, d);
     }
 }
 
@@ -861,10 +880,10 @@ AttnPlan plan_paged_attention(int64_t batch, int64_t n_q, int64_t n_kv, int64_t 
     return p;
 }
 
-void launch_paged_attention(const AttnArgs& a, int kind, int head_dim, hipStream_t st) {
-    if (kind == KV_F16)
+void launch_paged_attention(const AttnArgs& a, int head_dim, hipStream_t st) {
+    if (a.kind == KV_F16)
         launch_kind<KV_F16>(a, head_dim, st);
-    else if (kind == KV_BF16)
+    else if (a.kind == KV_BF16)
         launch_kind<KV_BF16>(a, head_dim, st);
     else
         launch_kind<KV_Q8>(a, head_dim, st);

@@ -233,8 +233,9 @@ struct AttnArgs {
     float scale_log2e;
     int2* meta;
     float* parts;
+    int kind;
 };
-void launch_paged_attention(const AttnArgs& a, int kind, int head_dim, hipStream_t st);
+void launch_paged_attention(const AttnArgs& a, int head_dim, hipStream_t st);
 
 // Residual addition and RMS norm of n rows of k; y (f32) or q and d (Q8_1).
 struct NormArgs {

@@ -954,7 +954,8 @@ int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int
     a.scale_log2e = scale * 1.4426950408889634f;
     a.meta = pl.ws_bytes > 0 ? (int2*)workspace : nullptr;
     a.parts = pl.ws_bytes > 0 ? (float*)((char*)workspace + pl.meta_bytes) : nullptr;
-    qmm::launch_paged_attention(a, cache->kind, (int)cache->head_dim, stream);
+    a.kind = cache->kind;
+    qmm::launch_paged_attention(a, (int)cache->head_dim, stream);
     return launch_status();
 }
 

@@ -44,3 +44,16 @@ def test_attention_far_value_scale_of_a_negligible_token(place, tokens):
         c["cache"].k_scale[page, h, at] = 60.0 / (c["scale"] * 100 * float(q.abs().sum()))
         c["cache"].v_scale[page, h, at] = 1e12 * float(c["cache"].v_scale[:, h].abs().max())
     _check(c)
+
+
+@pytest.mark.parametrize("tokens", [0, 9000])
+@pytest.mark.parametrize("q_mul,k_scale", [(0.0, 1.0), (1e34, 1e-36), (1e-34, 1e32), (1e-20, 1e18)])
+@pytest.mark.parametrize("v_scale", [1e30, 1e35, 1e-30])
+def test_attention_scales_near_the_f32_range(q_mul, k_scale, v_scale, tokens):
+    """Elements far from one on either side: outputs stay finite where elements and scores are."""
+    gh.note(f"attention q*{q_mul} key scales {k_scale} value scales {v_scale}, table for {tokens}")
+    c = _case("q8", [9000, 40, 1] if tokens else [150, 40, 1], 1, 2, 64, 16, q_mul=q_mul, stale=False)
+    c["cache"].k_scale.fill_(k_scale)
+    c["cache"].v_scale.fill_(v_scale)
+    c["cache"].v.abs_()
+    _check(c)
