@@ -13,10 +13,12 @@
 // Precision.  q and out are f32, and the arithmetic is f32's: an f32 operand
 // (q, p) is split into f16 parts (high and low, 22 bits; for a bf16 cache into
 // three bf16 parts, 24 bits), each multiplied with the cache's own 16-bit
-// values on v_mfma_f32_16x16x32 into the same f32 sum.  The parts keep their
+// values on v_mfma_f32_16x16x32 into the same f32 sum.  f16 parts keep their
 // bits because q is scaled to [2^13, 2^14) per head and p to (0, 2^14], powers
-// of two that cancel at the end.  8-bit rows are exact as f16 codes; a key's
-// scale multiplies its score, a value's scale its probability.
+// of two that cancel at the end; bf16 parts have f32's exponents and only stay
+// clear of its ends, keys and values reaching as far as f32's.  8-bit rows are
+// exact as f16 codes; a key's scale multiplies its score, a value's scale its
+// probability.
 //
 // Tiles.  A wave takes 32 tokens at a time: scores as K q^T (two 16-token
 // tiles: lane (c, i) = (lane / 16, lane % 16) gets head i's scores of tokens
@@ -114,12 +116,12 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
 }
 // One over what the weight of a head's largest score counts in its sums (m, l
 // and acc, in registers and in parts).  f16: 2^14, sums of values of at most
-// 65504 stay far inside f32.  8-bit elements are as large as their scales: 2^-b
+// 65504 stay far inside f32.  bf16 and 8-bit elements reach as far as f32: 2^-b
 // for up to 2^b tokens, so that a sum of weights times values is no larger than
 // the largest value.
+__device__ __forceinline__ int log2_up(int len) { return len > 1 ? 32 - __builtin_clz(len - 1) : 0; }
 __device__ __forceinline__ float one_weight(int kind, int len) {
-    if (kind != KV_Q8) return P_UNIT;
-    return fbits((uint32_t)(127 + (len > 1 ? 32 - __builtin_clz(len - 1) : 0)) << 23);
+    return kind == KV_F16 ? P_UNIT : fbits((uint32_t)(127 + log2_up(len)) << 23);
 }
 // A unit without tokens still takes one tile, whose wave writes its outputs.
 __device__ __forceinline__ int seq_tiles(int len) { return len <= TILE ? 1 : (len + TILE - 1) / TILE; }
@@ -314,6 +316,7 @@ struct Segment {
         const float* sb = Q8 ? ((lane & 32) ? a.v_scale : a.k_scale) + (int64_t)kvh * a.scale_head : nullptr;
         const int* table = a.table + (int64_t)b * a.table_stride;
         bool bad = false;
+        const float pbits = KIND == KV_BF16 ? (float)-log2_up(len) : PBITS;
 
         // page id of the lane's token (lane % 32) of tile tt; tokens behind the last read as the last
         auto token = [&](int tt) {
@@ -369,9 +372,18 @@ struct Segment {
             if (n > 1) id = page_id(t + 1);
             load_values();
             top = max_c(top);
-            // exponent field of 2^(13 - floor(log2 top)), kept normal with its inverse
-            int e = 267 - (int)(ubits(top) >> 23);
-            e = e > 253 ? 253 : (e < 1 ? 1 : e);
+            // q's factor, a power of two: its exponent field
+            int e;
+            if constexpr (KIND == KV_BF16) {
+                // 2^-12, so that the sum of products passes f32 no sooner than the score, but at
+                // least what takes the largest to 2^-60: its parts are normal numbers
+                e = 194 - (int)(ubits(top) >> 23);
+                e = e < 115 ? 115 : e;
+            } else {
+                // 2^(13 - floor(log2 top)), kept normal with its inverse
+                e = 267 - (int)(ubits(top) >> 23);
+                e = e > 253 ? 253 : (e < 1 ? 1 : e);
+            }
             const float f = fbits((uint32_t)e << 23);
             qs = fbits((uint32_t)(254 - e) << 23) * a.scale_log2e;
 #pragma unroll
@@ -424,7 +436,7 @@ struct Segment {
             float p[8], sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                p[j] = __builtin_amdgcn_exp2f(Q8 ? s[j] - base : s[j] - base + PBITS);
+                p[j] = __builtin_amdgcn_exp2f(Q8 ? s[j] - base : s[j] - base + pbits);
                 sum += p[j];
             }
             l = l * alpha + sum;
@@ -715,7 +727,7 @@ __device__ __forceinline__ Split split_of(const AttnArgs& a) {
     s.n = info.y == 0 ? 0 : info.y + 1;
     if (s.n) {
         s.u = unit_of(a, unit / a.batch, unit % a.batch);
-        s.unit = one_weight(a.kind, a.kind == KV_Q8 ? seq_len(a, s.u.b) : 1);
+        s.unit = one_weight(a.kind, a.kind == KV_F16 ? 1 : seq_len(a, s.u.b));
     }
     return s;
 }

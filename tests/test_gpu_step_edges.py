@@ -57,3 +57,15 @@ def test_attention_scales_near_the_f32_range(q_mul, k_scale, v_scale, tokens):
     c["cache"].v_scale.fill_(v_scale)
     c["cache"].v.abs_()
     _check(c)
+
+
+# ------------------------------------------------------------------ 16-bit ranges
+@pytest.mark.parametrize("tokens", [0, 9000])
+@pytest.mark.parametrize("q_mul,kv_mul", [(0.0, 3e37), (1e-35, 1e35), (1e-37, 3e37), (1e30, 1e-30), (1e34, 1e-34)])
+def test_attention_bf16_near_the_f32_range(q_mul, kv_mul, tokens):
+    """Finite keys and values up to the type's largest, with ordinary scores; every weight the same
+    (a q of zeros) makes the sum of weights times values the largest."""
+    gh.note(f"attention bf16 q*{q_mul} kv*{kv_mul}, table for {tokens}")
+    c = _case("bf16", [9000, 40, 1] if tokens else [150, 40, 1], 1, 2, 64, 16, q_mul=q_mul, kv_mul=kv_mul)
+    c["cache"].v.abs_()
+    _check(c)
