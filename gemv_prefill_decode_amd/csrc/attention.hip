@@ -74,7 +74,7 @@ constexpr int UNIT_START = 2, START_MIN = 6;
 constexpr float PBITS = 14.0f;
 constexpr float P_UNIT = 6.103515625e-05f;  // 2^-14
 constexpr int VEXP_MIN = 15;                // its inverse times 2^14 is a normal number
-constexpr float LN2 = 0.6931471805599453f;
+constexpr float LN2 = 0.6931471805599453f, LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ float fbits(uint32_t u) { return __builtin_bit_cast(float, u); }
@@ -385,7 +385,7 @@ struct Segment {
                 e = e > 253 ? 253 : (e < 1 ? 1 : e);
             }
             const float f = fbits((uint32_t)e << 23);
-            qs = fbits((uint32_t)(254 - e) << 23) * a.scale_log2e;
+            qs = fbits((uint32_t)(254 - e) << 23) * a.scale * LOG2E;  // scale * log2(e) may pass f32
 #pragma unroll
             for (int s = 0; s < NB; ++s) {
 #pragma unroll

@@ -230,7 +230,7 @@ struct AttnArgs {
     int blocks_per_kv, heads_per_block, cuts, groups;
     bool per_unit, meta_by_unit;
     int64_t head_spaces;
-    float scale_log2e;
+    float scale;
     int2* meta;
     float* parts;
     int kind;

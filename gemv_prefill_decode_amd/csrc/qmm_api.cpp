@@ -951,7 +951,7 @@ int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int
     a.meta_by_unit = pl.meta_by_unit;
     a.cuts = pl.cuts;
     a.head_spaces = pl.head_spaces;
-    a.scale_log2e = scale * 1.4426950408889634f;
+    a.scale = scale;
     a.meta = pl.ws_bytes > 0 ? (int2*)workspace : nullptr;
     a.parts = pl.ws_bytes > 0 ? (float*)((char*)workspace + pl.meta_bytes) : nullptr;
     a.kind = cache->kind;

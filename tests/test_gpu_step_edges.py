@@ -69,3 +69,10 @@ def test_attention_bf16_near_the_f32_range(q_mul, kv_mul, tokens):
     c = _case("bf16", [9000, 40, 1] if tokens else [150, 40, 1], 1, 2, 64, 16, q_mul=q_mul, kv_mul=kv_mul)
     c["cache"].v.abs_()
     _check(c)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8"])
+def test_attention_largest_scale(kind):
+    """A scale whose product with log2(e) passes the f32 range, on queries that bring the scores back."""
+    gh.note(f"attention {kind} scale 3e38")
+    _check(_case(kind, [70, 33, 1000], 2, 4, 64, 16, q_mul=1e-37, kv_mul=0.1, scale=3e38))
