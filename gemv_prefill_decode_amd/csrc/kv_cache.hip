@@ -161,19 +161,24 @@ __global__ __launch_bounds__(APP_THREADS) void kv_append_kernel(const AppendArgs
         const int64_t page = slot >> a.page_log2, in_page = slot & ((1 << a.page_log2) - 1);
         const int64_t at = page * a.page_stride + head * a.head_stride + in_page * a.slot_stride + 8 * e;
         if constexpr (KIND == KV_Q8) {
-            float top = 0.0f;
+            // The largest magnitude as bits: an infinity and then NaN are the largest of all, so
+            // that a row with either gets it as its scale and stays visible.
+            auto magnitude = [](float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; };
+            auto larger = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+            uint32_t bits = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(lo[j]), fabsf(hi[j])));
+            for (int j = 0; j < 4; ++j) bits = larger(bits, larger(magnitude(lo[j]), magnitude(hi[j])));
 #pragma unroll
-            for (int s = 1; s < LANES; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
-            float d = top / 127.0f;
+            for (int s = 1; s < LANES; s <<= 1) bits = larger(bits, (uint32_t)__shfl_xor((int)bits, s));
+            float d = __builtin_bit_cast(float, bits) / 127.0f;
             if (d < 1.17549435e-38f) d = 0.0f;  // its inverse would overflow
-            const float id = d != 0.0f ? 1.0f / d : 0.0f;
+            const bool finite = bits < 0x7f800000u;
+            const float id = finite && d != 0.0f ? 1.0f / d : 0.0f;
             uint32_t w[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                w[0] |= (uint32_t)(uint8_t)(int8_t)(int)roundf(lo[j] * id) << (8 * j);
-                w[1] |= (uint32_t)(uint8_t)(int8_t)(int)roundf(hi[j] * id) << (8 * j);
+                w[0] |= (uint32_t)(uint8_t)(int8_t)(int)roundf(finite ? lo[j] * id : 0.0f) << (8 * j);
+                w[1] |= (uint32_t)(uint8_t)(int8_t)(int)roundf(finite ? hi[j] * id : 0.0f) << (8 * j);
             }
             if (live) {
                 *(u32x2*)((int8_t*)(second ? a.vc : a.kc) + at) = u32x2{w[0], w[1]};

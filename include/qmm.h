@@ -516,8 +516,9 @@ int qmm_paged_extend(int32_t* block_table, int64_t table_stride, int32_t* seq_le
  * rounded to nearest even for QMM_KV_F16 and QMM_KV_BF16.  QMM_KV_Q8: per
  * row, in f32, d = max|x| / 127 (0 where that is below the smallest normal),
  * code = round-half-away-from-zero(x * (1/d)), or 0 when d = 0, as
- * qmm_quantize_q8_1 does per block.  A row with a NaN or an infinity has no
- * defined codes.
+ * qmm_quantize_q8_1 does per block.  A row with an infinity gets an infinite
+ * scale, one with a NaN a NaN (its codes are 0): attention over it is then
+ * non-finite in the heads that read it, as with the 16-bit kinds.
  *   k, v    DEVICE float, n rows of n_kv*head_dim, ldk and ldv floats apart
  *           (multiples of 4; rows of a fused projection's output), 16-byte
  *           aligned.

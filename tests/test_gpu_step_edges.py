@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 
 import gpu_helpers as gh
-from test_gpu_step import _case, _check, _torch
+from oracle import step
+from test_gpu_step import _case, _check, _new_cache, _qmm, _torch
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,31 @@ def test_attention_largest_scale(kind):
     """A scale whose product with log2(e) passes the f32 range, on queries that bring the scores back."""
     gh.note(f"attention {kind} scale 3e38")
     _check(_case(kind, [70, 33, 1000], 2, 4, 64, 16, q_mul=1e-37, kv_mul=0.1, scale=3e38))
+
+
+# ------------------------------------------------------------------ NaN and infinity
+@pytest.mark.parametrize("d", [32, 96, 128, 256])
+@pytest.mark.parametrize("bad", [np.nan, -np.nan, np.inf, -np.inf])
+def test_append_8bit_keeps_a_row_that_is_not_finite_visible(bad, d):
+    """One element of a key (then of a value) that is no number or infinite: its row's scale says
+    so, the head's attention is not finite, and no other row or head changes."""
+    torch, qmm = _torch(), _qmm()
+    gh.note(f"append q8 {bad} d={d}")
+    rng = np.random.default_rng(d)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for which in range(2):
+        rows = rng.normal(size=(2, 40, 3, d)).astype(np.float32)
+        rows[which, 17, 1, d - 3] = bad
+        cache, _ = _new_cache("q8", 3, 3, 16, d)
+        qmm.kv_append(cache, gh.to_dev(rows[0]), gh.to_dev(rows[1]), torch.arange(40, dtype=torch.int32, device="cuda"))
+        for i, (codes, scales) in enumerate(((cache.k, cache.k_scale), (cache.v, cache.v_scale))):
+            got, sc = (t.transpose(1, 2).flatten(0, 1)[:40].cpu().numpy() for t in (codes, scales))
+            want, ws = step.q8_rows(np.where(np.isfinite(rows[i]), rows[i], 0), d)
+            ws = ws[..., 0]
+            if i == which:
+                assert not got[17, 1].any() and (np.isnan(sc[17, 1]) if np.isnan(bad) else sc[17, 1] == np.inf)
+                got[17, 1], sc[17, 1] = want[17, 1], ws[17, 1]
+            assert np.array_equal(got, want) and np.array_equal(sc, ws)
+        q = gh.to_dev(rng.normal(size=(1, 6, d)).astype(np.float32))
+        out = qmm.paged_attention(q, cache, i32(0, 1, 2)[None], i32(40))[0].cpu().numpy()
+        assert not np.isfinite(out[2:4]).any() and np.isfinite(out[[0, 1, 4, 5]]).all()
