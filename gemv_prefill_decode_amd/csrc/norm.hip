@@ -30,17 +30,23 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 __device__ __forceinline__ float dot4(f32x4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
 
+__device__ __forceinline__ uint32_t code(float z, float id) { return (uint32_t)(uint8_t)(int8_t)(int)roundf(z * id); }
+
 // The Q8_1 codes of a block held by eight consecutive lanes, four values each.
+// The largest magnitude is taken as bits: an infinity and then NaN are the
+// largest of all, so that a block with either has it as its scale and codes 0.
 __device__ __forceinline__ uint32_t codes4(f32x4 z, float* d0) {
-    float top = fmaxf(fmaxf(fabsf(z.x), fabsf(z.y)), fmaxf(fabsf(z.z), fabsf(z.w)));
+    auto magnitude = [](float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; };
+    auto larger = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+    uint32_t bits = larger(larger(magnitude(z.x), magnitude(z.y)), larger(magnitude(z.z), magnitude(z.w)));
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
-    float dd = top / 127.0f;
+    for (int s = 1; s < 8; s <<= 1) bits = larger(bits, (uint32_t)__shfl_xor((int)bits, s));
+    float dd = __builtin_bit_cast(float, bits) / 127.0f;
     if (dd < 1.17549435e-38f) dd = 0.0f;  // its inverse would overflow
-    const float id = dd != 0.0f ? 1.0f / dd : 0.0f;
     *d0 = dd;
-    return (uint32_t)(uint8_t)(int8_t)(int)roundf(z.x * id) | ((uint32_t)(uint8_t)(int8_t)(int)roundf(z.y * id) << 8) |
-           ((uint32_t)(uint8_t)(int8_t)(int)roundf(z.z * id) << 16) | ((uint32_t)(uint8_t)(int8_t)(int)roundf(z.w * id) << 24);
+    const float id = dd != 0.0f ? 1.0f / dd : 0.0f;
+    const uint32_t codes = code(z.x, id) | code(z.y, id) << 8 | code(z.z, id) << 16 | code(z.w, id) << 24;
+    return bits < 0x7f800000u ? codes : 0;
 }
 
 template <bool NT>

@@ -597,7 +597,8 @@ int qmm_add_rmsnorm(float* y, int64_t ldy, float* h, int64_t ldh, const float* x
  * MoE projections).  1/rms is one factor of a whole row, so codes are those
  * of z = h * weight: per block of 32, in f32, d0 = max|z| / 127 (0 where that
  * is below the smallest normal), q = round-half-away-from-zero(z * (1/d0)),
- * or 0 when d0 = 0, and d = d0 / sqrt(mean h^2 + eps).
+ * or 0 when d0 = 0, and d = d0 / sqrt(mean h^2 + eps).  A block in which z has
+ * an infinity or a NaN has codes 0 and a d that is not finite.
  *   q     DEVICE int8[n*k], 16-byte aligned.  d: DEVICE float[n*k/32].
  *   k     a multiple of 32.
  * Other arguments as qmm_add_rmsnorm.

@@ -105,3 +105,25 @@ def test_append_8bit_keeps_a_row_that_is_not_finite_visible(bad, d):
         q = gh.to_dev(rng.normal(size=(1, 6, d)).astype(np.float32))
         out = qmm.paged_attention(q, cache, i32(0, 1, 2)[None], i32(40))[0].cpu().numpy()
         assert not np.isfinite(out[2:4]).any() and np.isfinite(out[[0, 1, 4, 5]]).all()
+
+
+@pytest.mark.parametrize("k", [32, 288, 1056, 4096, 20000])
+def test_norm_q8_keeps_what_is_not_finite_visible(k):
+    """A NaN or infinite weight shows in its block's scale alone; a NaN in x in all of its row's."""
+    torch, qmm = _torch(), _qmm()
+    gh.note(f"norm q8 not finite k={k}")
+    x, w = torch.randn(3, k, device="cuda"), torch.rand(k, device="cuda") + 0.5
+    good_q, good_d, _ = qmm.add_rmsnorm_q8(x, w)
+    for bad in (np.nan, -np.nan, np.inf, -np.inf):
+        for at in (0, k - 1):
+            wb = w.clone()
+            wb[at] = bad
+            q, d, _ = qmm.add_rmsnorm_q8(x, wb)
+            block = at // 32
+            assert not torch.isfinite(d[:, block]).any() and not q[:, 32 * block:32 * block + 32].any()
+            q[:, 32 * block:32 * block + 32], d[:, block] = good_q[:, 32 * block:32 * block + 32], good_d[:, block]
+            assert torch.equal(q, good_q) and torch.equal(d, good_d)
+    xb = x.clone()
+    xb[1, k // 2] = np.nan
+    q, d, _ = qmm.add_rmsnorm_q8(xb, w)
+    assert torch.isnan(d[1]).all() and torch.equal(d[::2], good_d[::2]) and torch.equal(q[::2], good_q[::2])
