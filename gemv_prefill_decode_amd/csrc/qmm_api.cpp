@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cerrno>
 #include <climits>
 #include <cstdlib>
@@ -341,6 +342,36 @@ int64_t strided_extent(const qmm_kv_cache* c, int64_t sp, int64_t sh, int64_t ss
     return p + h + s + row;
 }
 
+// Two arrays of [pages][heads][slots] rows of `row` bytes with the same strides
+// (bytes), `delta` bytes apart: whether a row of one meets a row of the other.
+// With a stride no smaller than what the smaller strides reach, as rows with
+// bytes of their own have, only two multiples of it leave a difference that
+// they can make up.
+struct Axis {
+    int64_t stride, count;
+};
+bool rows_meet(int64_t delta, int64_t row, const Axis* axes, int n) {
+    if (n == 0) return delta < row && -delta < row;
+    const int64_t s = axes[0].stride, q = delta / s - (delta % s < 0);  // rounded down
+    for (const int64_t a : {q, q + 1})
+        if (a < axes[0].count && -a < axes[0].count && rows_meet(delta - a * s, row, axes + 1, n - 1)) return true;
+    return false;
+}
+// From bases a and b, `bytes` from the first byte to the last; strides in elements of es bytes.
+bool arrays_meet(const void* a, const void* b, int64_t bytes, int64_t row, int64_t es, std::initializer_list<Axis> all) {
+    if (!overlap(a, bytes, b, bytes)) return false;
+    Axis axes[3];
+    int n = 0;
+    for (const Axis& x : all)
+        if (x.count > 1) axes[n++] = Axis{x.stride * es, x.count};
+    std::sort(axes, axes + n, [](const Axis& x, const Axis& y) { return x.stride > y.stride; });
+    return rows_meet((int64_t)((intptr_t)b - (intptr_t)a), row, axes, n);
+}
+// An array without gaps [a, a + bytes) holds the first or the last `row` bytes of another.
+bool holds_end(const void* a, int64_t bytes, const void* b, int64_t b_bytes, int64_t row) {
+    return overlap(a, bytes, b, row) || overlap(a, bytes, (const char*)b + (b_bytes - row), row);
+}
+
 int check_cache(const qmm_kv_cache* c, KvExtent* e) {
     if (!c || !c->k || !c->v) return QMM_ERR_NULL;
     if (c->kind != QMM_KV_F16 && c->kind != QMM_KV_BF16 && c->kind != QMM_KV_Q8) return QMM_ERR_QTYPE;
@@ -357,14 +388,17 @@ int check_cache(const qmm_kv_cache* c, KvExtent* e) {
         if (s % unit != 0) return QMM_ERR_ALIGN;
     }
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QMM_ERR_ALIGN;
-    if (c->k == c->v) return QMM_ERR_ALIAS;
     int64_t tokens;
     if (!mul_ok(c->n_pages, c->page_size, &tokens) || tokens > KV_TOKENS_MAX || c->n_kv > 65535) return QMM_ERR_RANGE;
     const int64_t elems = strided_extent(c, c->page_stride, c->head_stride, c->slot_stride, c->head_dim);
     // rows are addressed by a 32-bit count of 16-byte units from a head's first row
     if (elems < 0 || elems / unit >= ((int64_t)1 << 32)) return QMM_ERR_RANGE;
-    e->bytes = elems * (q8 ? 1 : 2);
+    const int64_t es = q8 ? 1 : 2;
+    e->bytes = elems * es;
     e->scale_bytes = 0;
+    if (arrays_meet(c->k, c->v, e->bytes, c->head_dim * es, es,
+                    {{c->page_stride, c->n_pages}, {c->head_stride, c->n_kv}, {c->slot_stride, c->page_size}}))
+        return QMM_ERR_ALIAS;
     if (q8) {
         for (const int64_t s : {c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride})
             if (s < 1) return QMM_ERR_SHAPE;
@@ -372,6 +406,18 @@ int check_cache(const qmm_kv_cache* c, KvExtent* e) {
         const int64_t sc = strided_extent(c, c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride, 1);
         if (sc < 0 || sc >= ((int64_t)1 << 40)) return QMM_ERR_RANGE;
         e->scale_bytes = sc * 4;
+        if (arrays_meet(c->k_scale, c->v_scale, e->scale_bytes, 4, 4,
+                        {{c->scale_page_stride, c->n_pages}, {c->scale_head_stride, c->n_kv},
+                         {c->scale_slot_stride, c->page_size}}))
+            return QMM_ERR_ALIAS;
+        // scales may lie between a page's codes, but not inside codes (nor codes inside scales)
+        // that leave no gaps
+        const int64_t rows = tokens * c->n_kv;
+        for (const void* codes : {c->k, c->v})
+            for (const void* scales : {c->k_scale, c->v_scale})
+                if ((elems == rows * c->head_dim && holds_end(codes, e->bytes, scales, e->scale_bytes, 4)) ||
+                    (sc == rows && holds_end(scales, e->scale_bytes, codes, e->bytes, c->head_dim)))
+                    return QMM_ERR_ALIAS;
     }
     return QMM_OK;
 }

@@ -453,11 +453,13 @@ typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8 = 2 } qmm_kv_kind;
  *     k[p*page_stride + h*head_stride + s*slot_stride + x]
  * and the same in v, so pages may hold heads outermost, tokens outermost, or
  * both caches in one tensor.  A token's slot number is p*page_size + s.
- *   k, v          16-byte aligned, not the same (QMM_ERR_ALIAS); strides in
- *                 elements, each >= head_dim and a multiple of 16 bytes, giving
- *                 every row bytes of its own.
+ *   k, v          16-byte aligned; strides in elements, each >= head_dim and a
+ *                 multiple of 16 bytes, giving every row bytes of its own: a
+ *                 row of k that meets one of v is QMM_ERR_ALIAS.
  *   k_scale, v_scale  QMM_KV_Q8 only (else ignored): float, strides in
- *                 elements, each >= 1.
+ *                 elements, each >= 1, giving every scale a place of its own
+ *                 (QMM_ERR_ALIAS where the two meet, or where either lies in
+ *                 codes that leave no gaps).
  *   page_size     a power of two.  head_dim: a multiple of 32, at most 256
  *                 (QMM_ERR_K_ALIGN, QMM_ERR_RANGE).
  * Limits (QMM_ERR_RANGE): n_pages*page_size <= 2^30, n_kv <= 65535, 64 GiB

@@ -155,3 +155,71 @@ def test_python_layer_refuses_host_tensors():
                  lambda: qmm.paged_extend(i[None].repeat(2, 1), i, i, i, 16, 2)):
         with pytest.raises(TypeError):
             call()
+
+
+# ------------------------------------------------------------------ arrays of a cache that meet
+def test_scales_and_codes_that_meet_are_refused():
+    """k_scale and v_scale the same, a part apart, or either inside codes (codes inside scales):
+    one call would write both."""
+    lib = _lib()
+    ks = P[2].value
+    for over in (dict(v_scale=ks), dict(v_scale=ks + 4), dict(v_scale=ks + 64 * 4), dict(v_scale=ks - 4),
+                 dict(v_scale=P[0].value), dict(k_scale=P[0].value + 1024), dict(k_scale=P[1].value - 4),
+                 dict(k_scale=P[1].value + 10 * 4096 - 4), dict(v_scale=P[1].value - 10 * 64 * 4 + 4),
+                 dict(v=P[0].value + 64), dict(v=P[0].value + 4096)):
+        c = ctypes.byref(_cache(2, **over))
+        assert lib.qmm_kv_append(c, P[4], 256, P[5], 256, P[6], 3, Z) == ALIAS, over
+        assert lib.qmm_paged_attention(P[4], 512, Z, P[5], 512, c, P[6], 8, P[7], 2, 8, 8, 0.1, P[8], 1 << 30, Z) == ALIAS, over
+
+
+def test_caches_whose_arrays_lie_between_each_other_are_taken():
+    """Keys and values of a page, of a head or of a token side by side, with or without their scales
+    behind them in one allocation (n = 0 is the refusal behind the cache's)."""
+    lib = _lib()
+    b, n_kv, page, d = P[0].value, 4, 16, 64
+
+    def taken(c):
+        return lib.qmm_kv_append(ctypes.byref(c), P[4], 256, P[5], 256, P[6], 0, Z) == SHAPE
+
+    rows = n_kv * page
+    assert taken(_cache(0, v=b + 2 * rows * d, page_stride=2 * rows * d))                                # per page
+    assert taken(_cache(0, v=b + 2 * page * d, page_stride=2 * rows * d, head_stride=2 * page * d))       # per head
+    assert taken(_cache(0, v=b + 2 * d, page_stride=2 * rows * d, head_stride=2 * page * d, slot_stride=2 * d))
+    assert taken(_cache(0, v=b + 2 * d, page_stride=2 * rows * d, slot_stride=2 * n_kv * d, head_stride=2 * d))
+    # 8 bits, one block a page: keys, values, key scales, value scales
+    block = 2 * rows * (d + 4)
+    for first in (0, 2 * rows * d):
+        assert taken(_cache(2, k=b + (0 if first else 8 * rows), v=b + (0 if first else 8 * rows) + rows * d,
+                            page_stride=block, k_scale=b + first, v_scale=b + first + 4 * rows,
+                            scale_page_stride=block // 4))
+    # one page: a stride that no second page has means nothing
+    assert taken(_cache(0, n_pages=1, page_stride=1 << 62)) and taken(_cache(2, n_pages=1, scale_page_stride=1 << 62))
+
+
+def test_keys_and_values_that_meet_are_found_exactly():
+    """Random layouts and distances against the set of the rows' bytes."""
+    import random
+    lib, rng = _lib(), random.Random(5)
+    seen = {True: 0, False: 0}
+    for _ in range(3000):
+        kind = rng.choice([0, 1, 2])
+        es, d = (1 if kind == 2 else 2), 32 * rng.randint(1, 2)
+        counts = dict(page=rng.randint(1, 4), head=rng.randint(1, 3), slot=rng.choice([1, 2, 4]))
+        strides, reach = {}, d
+        for axis in rng.sample(list(counts), 3):
+            strides[axis] = reach + 16 * rng.choice([0, 0, 1, 2, d // 16, reach // 16])
+            reach = strides[axis] * (counts[axis] - 1) + reach
+        delta = 16 * rng.randint(-reach * es // 16 - 1, reach * es // 16 + 1)
+        if rng.random() < 0.5:          # near a sum of strides
+            delta = sum(s * es * rng.randint(-1, 1) for s in strides.values()) + 16 * rng.randint(-1, 1)
+        offsets = [es * (p * strides["page"] + h * strides["head"] + s * strides["slot"])
+                   for p in range(counts["page"]) for h in range(counts["head"]) for s in range(counts["slot"])]
+        mine = {o // 16 + i for o in offsets for i in range(d * es // 16)}
+        meet = any(o // 16 + i + delta // 16 in mine for o in offsets for i in range(d * es // 16))
+        c = _cache(kind, v=P[0].value + delta, n_pages=counts["page"], n_kv=counts["head"], page_size=counts["slot"],
+                   head_dim=d, page_stride=strides["page"], head_stride=strides["head"], slot_stride=strides["slot"],
+                   scale_page_stride=100, scale_head_stride=10, scale_slot_stride=1)
+        got = lib.qmm_kv_append(ctypes.byref(c), P[4], 256, P[5], 256, P[6], 0, Z)
+        assert got == (ALIAS if meet else SHAPE), (kind, d, counts, strides, delta)
+        seen[meet] += 1
+    assert min(seen.values()) > 300
