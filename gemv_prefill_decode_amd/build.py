@@ -89,21 +89,27 @@ def build(verbose: bool = False) -> str:
 
 def build_step() -> str:
     """The Python module of the decode step's calls (checks torch tensors and
-    calls the library through addresses it is given): host code only."""
+    calls the library through addresses it is given): host code only, by the
+    same compiler.  Without torch there is nothing to bind: the C library is
+    whole without it, and "" is returned."""
     import sysconfig
 
-    import torch
-    from torch.utils import cpp_extension
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        sys.stderr.write(f"no torch ({e}): the Python module _step.so is not built\n")
+        return ""
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(rocm_home(), "include")]
     tmp = STEP_OUT + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+    cmd = [hipcc(), "-no-hip-rt", "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
     cmd += [x for i in inc for x in ("-isystem", i)]
     cmd += [os.path.join(CSRC, "step_bind.cpp"), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for step_bind.cpp:\n" + r.stdout + r.stderr)
+        raise RuntimeError("hipcc failed for step_bind.cpp:\n" + r.stdout + r.stderr)
     os.replace(tmp, STEP_OUT)
     return STEP_OUT
 
