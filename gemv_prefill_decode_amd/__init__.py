@@ -634,6 +634,8 @@ def _load_step():
 
 def _run(f, dev, stream, *args):
     """f on device dev, on the given stream or the device's current one."""
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on device {dev}")
     if stream is None and _current_device() == dev:
         st = f(_current_stream(dev), dev, *args)
     else:

@@ -127,3 +127,25 @@ def test_norm_q8_keeps_what_is_not_finite_visible(k):
     xb[1, k // 2] = np.nan
     q, d, _ = qmm.add_rmsnorm_q8(xb, w)
     assert torch.isnan(d[1]).all() and torch.equal(d[::2], good_d[::2]) and torch.equal(q[::2], good_q[::2])
+
+
+# ------------------------------------------------------------------ streams
+def test_a_stream_of_another_device_is_refused():
+    """Every call with all outputs given; a stream that says it belongs to device 1."""
+    torch, qmm = _torch(), _qmm()
+
+    class Other:
+        device_index, cuda_stream = 1, 0
+        device = torch.device("cuda", 0)
+
+    c = _case("f16", [20], 1, 1, 32, 16, stale=False)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    x, out, rows = torch.zeros(2, 32, device="cuda"), torch.full((2, 32), 5.0, device="cuda"), i32(7, 7)
+    for call in (lambda: qmm.kv_append(c["cache"], x, x, rows, stream=Other()),
+                 lambda: qmm.add_rmsnorm(x, x[0], y=out, stream=Other()),
+                 lambda: qmm.paged_extend(rows[None], i32(0), i32(1), i32(0), 16, 1, rows[:1], rows[1:], i32(0), i32(0),
+                                          stream=Other())):
+        with pytest.raises(ValueError, match="device 1"):
+            call()
+    torch.cuda.synchronize()
+    assert (out == 5).all() and (rows == 7).all()

@@ -223,3 +223,12 @@ def test_keys_and_values_that_meet_are_found_exactly():
         assert got == (ALIAS if meet else SHAPE), (kind, d, counts, strides, delta)
         seen[meet] += 1
     assert min(seen.values()) > 300
+
+
+def test_python_layer_refuses_a_stream_of_another_device():
+    import types
+    import gemv_prefill_decode_amd as qmm
+    called = []
+    with pytest.raises(ValueError, match="device 1"):
+        qmm._run(called.append, 0, types.SimpleNamespace(device_index=1, cuda_stream=0))
+    assert not called
