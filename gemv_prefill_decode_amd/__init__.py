@@ -715,12 +715,13 @@ def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=No
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a tensor")
         workspace = True
-        if stream is not None:
-            import torch
-            n = paged_attention_workspace_bytes(seq_lens.shape[0], q[0].numel() // cache.head_dim, cache,
-                                                block_table.shape[1])
-            workspace = _new(n, torch.uint8, q, stream) if n > 0 else None
-    _run(step.paged_attention, cache._index, stream, cache._ptr, q, block_table, seq_lens, scale, out, lse, workspace)
+    args = (cache._ptr, q, block_table, seq_lens, scale, out, lse, workspace)
+    if stream is None:
+        _run(step.paged_attention, cache._index, stream, *args)
+    else:
+        import torch
+        with torch.cuda.stream(stream):     # the workspace is allocated on it
+            _run(step.paged_attention, cache._index, stream, *args)
     return out
 
 

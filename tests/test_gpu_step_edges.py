@@ -149,3 +149,17 @@ def test_a_stream_of_another_device_is_refused():
             call()
     torch.cuda.synchronize()
     assert (out == 5).all() and (rows == 7).all()
+
+
+def test_attention_of_no_sequences_is_the_same_refusal_on_any_stream():
+    torch, qmm = _torch(), _qmm()
+    c = _case("f16", [20], 1, 2, 32, 16, stale=False)
+    table, lens = torch.zeros(0, 4, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        for q in (c["q"][:0], c["q"][:0].flatten(1)):
+            with pytest.raises(qmm.QmmError) as e:
+                qmm.paged_attention(q, c["cache"], table, lens, stream=stream)
+            assert e.value.status == 1      # an empty tensor has no address, and that is checked first
+        with pytest.raises(ValueError):
+            qmm.paged_attention(c["q"].flatten(), c["cache"], table, lens, stream=stream)
+    torch.cuda.synchronize()
