@@ -716,7 +716,7 @@ def paged_attention(q, cache: KVCache, block_table, seq_lens, scale=None, out=No
             raise ValueError("workspace must be 'auto', None or a tensor")
         workspace = True
     args = (cache._ptr, q, block_table, seq_lens, scale, out, lse, workspace)
-    if stream is None:
+    if stream is None or workspace is not True:
         _run(step.paged_attention, cache._index, stream, *args)
     else:
         import torch

@@ -163,3 +163,19 @@ def test_attention_of_no_sequences_is_the_same_refusal_on_any_stream():
         with pytest.raises(ValueError):
             qmm.paged_attention(c["q"].flatten(), c["cache"], table, lens, stream=stream)
     torch.cuda.synchronize()
+
+
+def test_attention_with_own_outputs_takes_any_stream_handle():
+    """Nothing is allocated for the call: a stream known by its handle alone will do."""
+    import types
+    torch, qmm = _torch(), _qmm()
+    c = _case("f16", [300, 40], 2, 4, 64, 16, stale=False, tokens=4000)
+    args = (c["q"], c["cache"], torch.from_numpy(c["table"]).cuda(),
+            torch.tensor(c["lens"], dtype=torch.int32, device="cuda"))
+    need = qmm.paged_attention_workspace_bytes(2, 8, c["cache"], args[2].shape[1])
+    out, ws, side = torch.empty_like(c["q"]), torch.empty(need, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    want = qmm.paged_attention(*args)
+    torch.cuda.synchronize()
+    qmm.paged_attention(*args, out=out, workspace=ws, stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
+    side.synchronize()
+    assert need > 0 and torch.equal(out, want)
