@@ -97,8 +97,11 @@ def rmsnorm(h, w, eps: float):
 
 
 def rmsnorm_rel(k: int) -> float:
-    """Relative bound of an f32 evaluation with u = 2^-24: the sum of k squares in up to 512 partial
-    sums of at most 16 * ceil(k / 16384) terms (each square and addition one rounding, 10 more to
-    join), halved by the root; mean, eps, root, inverse and the two products 7 more."""
+    """Relative bound of an f32 evaluation with u = 2^-24.  No square goes through more than
+    16 * ceil(k / 16384) + 12 roundings on its way into the sum: with 1024 threads a row, in passes
+    P = ceil(k / 16384) of four times four elements a thread, its own, 3 for the others of its four,
+    4P - 1 for the thread's, 6 for the wave's lanes and 15 for the 16 waves, 24 + 4P in all; with 256
+    threads and up to eight times four elements 1 + 3 + 7 + 6 + 3.  The root halves them; mean, eps,
+    root, inverse and the two products add at most 7."""
     terms = 16 * math.ceil(k / 16384) + 12
     return (terms / 2 + 7) * 2.0 ** -24

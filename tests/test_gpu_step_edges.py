@@ -179,3 +179,96 @@ def test_attention_with_own_outputs_takes_any_stream_handle():
     qmm.paged_attention(*args, out=out, workspace=ws, stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
     side.synchronize()
     assert need > 0 and torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ norm
+def _norm_inputs(n, k, residual, seed):
+    rng = np.random.default_rng(seed)
+    x, r, w = (rng.normal(size=s).astype(np.float32) for s in ((n, k), (n, k), (k,)))
+    return x, r if residual else None, w
+
+
+def _check_norm_rows(rows, x, r, w, y=None, q=None, d=None, h=None):
+    """Rows of a norm's outputs against the oracle (x, r, w host arrays of all rows)."""
+    hs = x[rows] if r is None else x[rows] + r[rows]
+    want, inv = step.rmsnorm(hs, w, 1e-5)
+    rel = step.rmsnorm_rel(hs.shape[1])
+    if h is not None:
+        assert np.array_equal(h[rows].cpu().numpy(), hs)
+    if y is not None:
+        assert (np.abs(y[rows].cpu().double().numpy() - want) <= rel * np.abs(want) + 1e-44).all()
+    else:
+        codes, d0 = step.q8_rows(hs * w, 32)
+        assert np.array_equal(q[rows].cpu().numpy(), codes)
+        assert (np.abs(d[rows].cpu().double().numpy() - d0 * inv) <= rel * d0 * inv).all()
+
+
+# 257 rows are more than the device's CUs: 256 threads a row with 2 to 8 elements of four each, then 1024
+NORM_WIDTHS = [1028, 1056, 2048, 2052, 2080, 3104, 4096, 4608, 5120, 5124, 6176, 7168, 7200, 8192, 8196, 8224, 16384, 16416]
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("k", NORM_WIDTHS)
+def test_norm_of_more_rows_than_cus(k, residual):
+    qmm = _qmm()
+    gh.note(f"norm n=257 k={k} residual={residual}")
+    x, r, w = _norm_inputs(257, k, residual, k)
+    dev = [None if v is None else gh.to_dev(v) for v in (x, w, r)]
+    rows = np.arange(257)
+    y, h = qmm.add_rmsnorm(*dev)
+    _check_norm_rows(rows, x, r, w, y=y, h=h)
+    if k % 32 == 0:
+        q, d, h = qmm.add_rmsnorm_q8(*dev)
+        _check_norm_rows(rows, x, r, w, q=q, d=d, h=h)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("k", [1024, 2048, 2080, 4096, 4608, 6144, 7168, 8192, 12288])
+def test_norm_of_large_inputs(k, residual):
+    """More than 48 MB of input, read past the caches: rows against the oracle, and all of them equal
+    to calls of 300 rows each, which are not (fewer rows than CUs would add in another order)."""
+    torch, qmm = _torch(), _qmm()
+    n = (50 << 20) // (k * (8 if residual else 4)) + 2
+    gh.note(f"norm n={n} k={k} residual={residual}")
+    x, r, w = _norm_inputs(n, k, residual, k)
+    dx, dw, dr = (None if v is None else gh.to_dev(v) for v in (x, w, r))
+    rows = np.unique(np.concatenate([[0, 1, n - 2, n - 1], np.random.default_rng(1).integers(0, n, 60)]))
+    for f in (qmm.add_rmsnorm, qmm.add_rmsnorm_q8):
+        got = f(dx, dw, dr)
+        _check_norm_rows(rows, x, r, w, **dict(zip(("y", "h") if len(got) == 2 else ("q", "d", "h"), got)))
+        for at in [*range(0, n - 300, 300), n - 300]:
+            part = f(dx[at:at + 300], dw, None if dr is None else dr[at:at + 300])
+            assert all(g is None or torch.equal(g[at:at + 300], p) for g, p in zip(got, part))
+
+
+# ------------------------------------------------------------------ steps at the same time
+def test_whole_steps_at_the_same_time_on_three_streams():
+    """Page tables, append, attention and norm of three caches on three streams, without waiting between
+    them: both equal their serial results."""
+    torch, qmm = _torch(), _qmm()
+    cases = [_case(k, [2500, 40, 0, 900], 4, 2, 64, 16, seed=s, tokens=4000, stale=False)
+             for s, k in ((3, "f16"), (4, "q8"), (5, "bf16"))]
+    w = torch.ones(512, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def one(c, stream=None):
+        lens, slots, pos, used = qmm.paged_extend(c["tab"], c["cached"], c["new"], c["free"], 16, 6, stream=stream)
+        qmm.kv_append(c["cache"], c["rows"][0], c["rows"][1], slots, stream=stream)
+        out = qmm.paged_attention(c["q"], c["cache"], c["tab"], lens, stream=stream)
+        y, h = qmm.add_rmsnorm(out.flatten(1), w, out.flatten(1), stream=stream)
+        return lens, slots, pos, used, out, y, h
+
+    for c in cases:                     # the last token of each sequence is the step's new one
+        c["tab"] = torch.from_numpy(c["table"]).cuda()
+        c["cached"], c["new"] = i32([2499, 39, 0, 899]), i32([1, 1, 0, 1])
+        c["free"] = i32([0, 1])         # never needed: those tokens' pages are there
+        c["rows"] = torch.randn(2, 6, 4, 64, device="cuda")
+        c["want"] = [t.clone() for t in one(c)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        got = [one(c, s) for c, s in zip(cases, streams)]
+        for s in streams:
+            s.synchronize()
+        for c, g in zip(cases, got):
+            assert c["want"][3].item() == 0 and all(torch.equal(x, y) for x, y in zip(g, c["want"]))
