@@ -73,7 +73,6 @@ constexpr int occupancy(int kind, int nb) { return nb <= (kind == KV_Q8 ? 6 : 5)
 constexpr int UNIT_START = 2, START_MIN = 6;
 constexpr float PBITS = 14.0f;
 constexpr float P_UNIT = 6.103515625e-05f;  // 2^-14
-constexpr int VEXP_MIN = 15;                // its inverse times 2^14 is a normal number
 constexpr float LN2 = 0.6931471805599453f, LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -211,8 +210,8 @@ struct Segment {
     f32x4 acc[2 * NB];
     float m, l;
     // 8-bit values: the largest weight times value scale so far, against the
-    // present maximum, and the exponent field of a power of two above it, which
-    // acc's sums are relative to
+    // present maximum, and the exponent of a power of two above it, which acc's
+    // sums are relative to
     float vtop;
     int vexp;
 
@@ -304,7 +303,7 @@ struct Segment {
         m = -INFINITY;
         l = 0.0f;
         vtop = 0.0f;
-        vexp = VEXP_MIN;
+        vexp = 0;
 #pragma unroll
         for (int o = 0; o < 2 * NB; ++o) acc[o] = f32x4{0, 0, 0, 0};
         if (len <= 0) {
@@ -316,7 +315,7 @@ struct Segment {
         const float* sb = Q8 ? ((lane & 32) ? a.v_scale : a.k_scale) + (int64_t)kvh * a.scale_head : nullptr;
         const int* table = a.table + (int64_t)b * a.table_stride;
         bool bad = false;
-        const float pbits = KIND == KV_BF16 ? (float)-log2_up(len) : PBITS;
+        const float pbits = KIND == KV_BF16 ? (float)-log2_up(len) : Q8 ? 0.0f : PBITS;
 
         // page id of the lane's token (lane % 32) of tile tt; tokens behind the last read as the last
         auto token = [&](int tt) {
@@ -431,12 +430,14 @@ struct Segment {
             for (int j = 1; j < 8; ++j) top = fmaxf(top, s[j]);
             top = fmaxf(m, max_c(top));
             const float base = top == -INFINITY ? 0.0f : top;
+            const float shift = base - pbits;
             float alpha = __builtin_amdgcn_exp2f(m - base);
             m = top;
             float p[8], sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                p[j] = __builtin_amdgcn_exp2f(Q8 ? s[j] - base : s[j] - base + pbits);
+                // f16's offset apart from the maximum
+                p[j] = __builtin_amdgcn_exp2f(KIND == KV_F16 ? s[j] - base + pbits : s[j] - shift);
                 sum += p[j];
             }
             l = l * alpha + sum;
@@ -452,16 +453,12 @@ struct Segment {
                     big = fmaxf(big, fabsf(p[j]));
                 }
                 vtop = fmaxf(vtop * alpha, max_c(big));
-                int e = (int)(ubits(vtop) >> 23) + 1;
-                e = e < VEXP_MIN ? VEXP_MIN : (e > 254 ? 254 : e);
-                int step = 127 + vexp - e;
-                step = step < 0 ? 0 : (step > 254 ? 254 : step);
-                alpha *= fbits((uint32_t)step << 23);
+                const int e = __builtin_amdgcn_frexp_expf(vtop);
+                alpha = __builtin_amdgcn_ldexpf(alpha, vexp - e);
                 vexp = e;
-                const float inv = fbits((uint32_t)(127 + 14 + 127 - e) << 23);  // to at most 2^14
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    p[j] *= inv;
+                    p[j] = __builtin_amdgcn_ldexpf(p[j], 14 - e);
                     // The product as one f32 value: the compiler otherwise rounds it to f16 for the
                     // high part straight from its factors (v_fma_mixlo_f16), which near a tie is not
                     // the f16 that the low part was taken against (2^-11 off, seen about once in 10^4).
@@ -487,7 +484,9 @@ struct Segment {
         if constexpr (Q8) {
             const float u = 1.0f / one_weight(KIND, len);
 #pragma unroll
-            for (int o = 0; o < 2 * NB; ++o) acc[o] = acc[o] * (P_UNIT * u) * fbits((uint32_t)vexp << 23);
+            for (int o = 0; o < 2 * NB; ++o)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[o][r] = __builtin_amdgcn_ldexpf(acc[o][r] * (P_UNIT * u), vexp);
             l *= u;
         }
     }
@@ -601,7 +600,7 @@ template <int KIND, int NB>
 __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(const AttnArgs a) {
     constexpr int D = 32 * NB;
     extern __shared__ __attribute__((aligned(16))) float parts[];  // [wave][2] parts
-    __shared__ int part_unit[4][2], part_ends[4][2];
+    __shared__ int part_unit[4][2], part_ends[4][2], part_len[4][2];
     __shared__ int2 out_unit;  // the unit that starts here and goes on in the next work groups, and in how many
     const int tid = threadIdx.x, w = uni(tid >> 6), lane = tid & 63;
     const int g = blockIdx.x;
@@ -655,6 +654,7 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
             if (lane == 0) {
                 part_unit[w][slot] = hs * a.batch + b;
                 part_ends[w][slot] = t + n == nt;
+                part_len[w][slot] = len;
             }
         }
         if (t == 0 && !a.per_unit) {  // work groups after this one that share the unit
@@ -674,6 +674,9 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
     // Join the parts of each unit, in token order: a unit that starts here
     // (slot 1 of some wave) or came in from the previous work group (slot 0 of
     // wave 0), and the slots 0 of the following waves up to its end.
+    // (Unrolled: left to itself the compiler rolls it for bf16 and 8-bit rows, 0.1
+    // us more per call for 97 tokens, 0.6 for 64 sequences of 2048.)
+#pragma unroll
     for (int first = -1; first < 4; ++first) {
         const int w0 = first < 0 ? 0 : first, s0 = first < 0 ? 0 : 1;
         const int unit = part_unit[w0][s0];
@@ -700,7 +703,7 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
             }
             if (whole) {
                 *(f32x4*)(a.out + (int64_t)u.b * a.out_stride + (int64_t)(u.head0 + row) * D + d) = o * (1.0f / l);
-                if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l, one_weight(KIND, seq_len(a, u.b)));
+                if (a.lse && d == 0) a.lse[(int64_t)u.b * a.n_q + u.head0 + row] = lse_of(top, l, one_weight(KIND, part_len[w0][s0]));
             } else {
                 *(f32x4*)(ws + row * D + d) = o;
                 if (d == 0) *(f32x2*)(ws + a.heads_per_block * D + 2 * row) = f32x2{top, l};
