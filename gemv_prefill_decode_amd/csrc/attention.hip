@@ -42,12 +42,12 @@
 // faster: release fences write back whole L2s, 171 us for 96; device-scope
 // stores and a counter took the 9 us that the second kernel had taken.)
 //
-// Measured (MI355X, 8 kv heads of 128): 131071 tokens of f16, 537 MB, 88 us
-// (6.1 TB/s; a kernel that only reads reaches 7.0); 51 sequences of up to
-// 16384 tokens of bf16, tokens outermost, 1109 MB, 190 us (5.8 TB/s); 64
-// sequences of up to 8192 8-bit tokens, 382 MB, 74 us (5.1 TB/s; vector ALUs
-// 55% busy with the codes' conversion); one sequence of 97 tokens, heads of
-// 64, 5.7 us (launch and four dependent loads).
+// Measured (MI355X, 8 kv heads of 128; both kernels): 131071 tokens of f16, 537
+// MB, 89 us (6.0 TB/s; a kernel that only reads reaches 7.0); 51 sequences of up
+// to 16384 tokens of bf16, tokens outermost, 1109 MB, 188 us (5.9 TB/s); 64
+// sequences of up to 8192 8-bit tokens, 382 MB, 72 us (5.3 TB/s; vector ALUs
+// about half busy, most of it the codes' conversion); one sequence of 97 tokens,
+// heads of 64, 5.1 us (launch and four dependent loads).
 #include "common.hpp"
 #include "kernels.hpp"
 

@@ -15,7 +15,7 @@ namespace {
 // without communication between work groups: each scans all sequences in
 // passes of THREADS (two sums), and writes its own range of rows and its
 // stride of new table entries, which it finds in the pass by bisection.
-// Measured: 64 sequences of one new token 3.2 us, 512 prompts with 88600 rows
+// Measured: 64 sequences of one new token 2.9 us, 512 prompts with 88600 rows
 // 3.9, 1024 prompts on pages of one token 5.2 (with 64-bit sums, LDS shuffles
 // and a branching bisection 4.0, 7.0 and 13.0; a launch alone 1.6).
 //
@@ -132,8 +132,9 @@ __global__ __launch_bounds__(THREADS) void paged_extend_kernel(const ExtendArgs 
 // head_dim / 8 is none, which find the row's largest magnitude together.
 // Measured: 8192 tokens of 8 heads of 128 from f32 to bf16, 100.7 MB, 18.6 us
 // where the projection's output is still in the 256 MB cache (5.4 TB/s), 22 us
-// from HBM (4.5; a copy reaches 4.7); 16 tokens 2.0 us.  Non-temporal loads
-// gain 1 us of the 22 and lose 4 of the others: not used.
+// from HBM (4.5; a copy reaches 4.7); 16 tokens 2.8 us.  To 8 bits 17.6 us (84.4
+// MB, 4.8 TB/s) and 3.2.  Non-temporal loads gain 1 us of the 22 and lose 4 of
+// the others: not used.
 constexpr int APP_THREADS = 256;
 
 template <int KIND, int NB>

@@ -127,11 +127,13 @@ __global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(const NormArgs a) 
 template <int THREADS, int T, int V, bool LOOP = false>
 void launch(const NormArgs& all, hipStream_t st) {
     constexpr int ROWS = THREADS / T;
-    // Large inputs are read past the caches: from HBM 2048 x 4096 takes 23.1 us
-    // (else 24.2), 2048 x 4608 26.0 (33.8), 512 x 14336 20.5 (27.5), 2048 x 4096
-    // to Q8_1 23.5 (28.0).  Inputs that the 256 MB cache behind the L2s still
-    // holds from their producer lose by it (2048 x 4096 26.3 against 23.7, 1000
-    // x 4608 to Q8_1 15.5 against 14.8), so only those of over 48 MB.
+    // Large inputs are read past the caches.  Kernel times so (and through them)
+    // with x and the residual just written, with x just written, and with neither,
+    // behind 640 MB of other writes: 2048 x 4096 19.0 us (19.2), 20.3 (24.8), 23.0
+    // (35.0); 512 x 14336 16.8 (17.2), 18.1 (23.0), 20.0 (31.5); 8192 x 4096 83.9
+    // (101.7), 81.9 (99.4), 101.4 (123.9); Q8_1 the same within 10%.  Below 48 MB
+    // it gains from HBM and loses a little where the 256 MB cache behind the L2s
+    // holds all: 1000 x 4608 13.6 (13.0), 12.4 (14.9), 13.4 (20.3).
     const bool nt = !LOOP && all.n * all.k * (all.r ? 8 : 4) > ((int64_t)48 << 20);
     // a launch has fewer than 2^32 threads
     constexpr int64_t MOST = ((int64_t)1 << 31) / THREADS * ROWS;

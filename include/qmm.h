@@ -549,7 +549,9 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * f32 range.
  * f32 arithmetic: f32 operands enter the matrix cores as two f16 (three
  * bf16) parts, products and sums are f32; the exponential and logarithm are
- * the hardware's.
+ * the hardware's.  (f16 parts: an element of q is kept to 2^-38 of its head's
+ * largest, a weight to 2^-39 of the largest.)  Finite elements and scores
+ * give finite outputs.
  *   out   DEVICE float, rows ldo >= n_q*head_dim apart (a multiple of 4),
  *         16-byte aligned.  lse: DEVICE float[batch*n_q] or NULL.
  *   q     DEVICE float, rows ldq apart (as ldo), 16-byte aligned.
