@@ -9,6 +9,9 @@ streams.
     out = gemm(w, x, m, "q4_k")            # dst[n, m] = x[n, k] @ deq(w)[m, k]^T
     g, u = moe_gateup(wg, wu, ids, scales, x, n_expert, n_ff, "nvfp4")
 
+    q, e = quantize_mxfp4(x)               # 4-bit floats with a scale per 32
+    out = gemm_mxfp4(wq, we, q, e)         # both sides in MXFP4
+
 and, between a decode step's projections,
 
     y, h = add_rmsnorm(x, weight, residual)
@@ -34,12 +37,13 @@ __all__ = [
     "stream_loadonly", "repack_nvfp4_v2", "quantize_q8_1", "moe_gateup_q8",
     "KV_KINDS", "KVCache", "paged_extend", "kv_append", "paged_attention", "paged_attention_workspace_bytes",
     "add_rmsnorm", "add_rmsnorm_q8",
+    "quantize_mxfp4", "dequantize_mxfp4", "gemm_mxfp4", "add_rmsnorm_mxfp4",
     "row_bytes", "block_elems", "gemv_max_n", "status_str", "abi_version",
 ]
 
 QTYPES = {"f32": 0, "q4_0": 1, "q8_0": 2, "q4_k": 3, "q6_k": 4, "nvfp4": 5, "nvfp4_v2": 6}
 PATHS = {"auto": 0, "gemv": 1, "mfma": 2, "gemv_fma": 3, "gemv_matrix": 4}
-KV_KINDS = {"f16": 0, "bf16": 1, "q8": 2}
+KV_KINDS = {"f16": 0, "bf16": 1, "q8": 2, "mxfp4": 4}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -120,6 +124,14 @@ def load() -> ctypes.CDLL:
         lib.qmm_add_rmsnorm.restype = i32
         lib.qmm_add_rmsnorm_q8.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, f32, vp]
         lib.qmm_add_rmsnorm_q8.restype = i32
+        lib.qmm_add_rmsnorm_mxfp4.argtypes = [vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, i64, f32, vp]
+        lib.qmm_add_rmsnorm_mxfp4.restype = i32
+        lib.qmm_quantize_mxfp4.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp]
+        lib.qmm_quantize_mxfp4.restype = i32
+        lib.qmm_dequantize_mxfp4.argtypes = [vp, vp, vp, i64, i64, vp]
+        lib.qmm_dequantize_mxfp4.restype = i32
+        lib.qmm_gemm_mxfp4.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, vp]
+        lib.qmm_gemm_mxfp4.restype = i32
         lib.qmm_row_bytes.argtypes = [i32, i64]
         lib.qmm_row_bytes.restype = i64
         lib.qmm_block_elems.argtypes = [i32]
@@ -551,16 +563,18 @@ class KVCache:
     device memory, which the object keeps alive, in any order of pages, heads and tokens with unit
     stride along head_dim (pages that hold tokens outermost: ``pages.transpose(1, 2)``).
 
-    float16 or bfloat16, or int8 codes with k_scale and v_scale float32 [n_pages, n_kv, page_size].
+    float16 or bfloat16, or int8 codes with k_scale and v_scale float32 [n_pages, n_kv, page_size], or
+    MXFP4: uint8 codes [n_pages, n_kv, page_size, head_dim/2] with uint8 scales
+    [n_pages, n_kv, page_size, head_dim/32] (as quantize_mxfp4 gives them).
     page_size: a power of two; head_dim: a multiple of 32 up to 256."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        kinds = {torch.float16: "f16", torch.bfloat16: "bf16", torch.int8: "q8"}
+        kinds = {torch.float16: "f16", torch.bfloat16: "bf16", torch.int8: "q8", torch.uint8: "mxfp4"}
         if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or not k.is_cuda or not v.is_cuda:
             raise TypeError("k and v must be device (cuda/hip) tensors")
         if k.dtype not in kinds or v.dtype != k.dtype:
-            raise TypeError(f"k and v must both be float16, bfloat16 or int8, got {k.dtype} and {v.dtype}")
+            raise TypeError(f"k and v must both be float16, bfloat16, int8 or uint8, got {k.dtype} and {v.dtype}")
         if k.dim() != 4 or k.shape != v.shape:
             raise ValueError("k and v must both be [n_pages, n_kv, page_size, head_dim]")
         self.kind = kinds[k.dtype]
@@ -568,8 +582,8 @@ class KVCache:
         if strides != _view_strides(v, 3, "v"):
             raise ValueError("k and v must have the same strides")
         scale_strides = (1, 1, 1)
-        if (k_scale is not None or v_scale is not None) != (self.kind == "q8"):
-            raise ValueError("k_scale and v_scale belong to an int8 cache")
+        if (k_scale is not None or v_scale is not None) != (self.kind in ("q8", "mxfp4")):
+            raise ValueError("k_scale and v_scale belong to an int8 or uint8 cache")
         if self.kind == "q8":
             for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
                 if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
@@ -579,16 +593,28 @@ class KVCache:
             scale_strides = _view_strides(k_scale, 3, "k_scale", 1)
             if scale_strides != _view_strides(v_scale, 3, "v_scale", 1):
                 raise ValueError("k_scale and v_scale must have the same strides")
+        shape = tuple(k.shape)
+        if self.kind == "mxfp4":
+            shape = shape[:3] + (2 * shape[3],)
+            strides = tuple(2 * s for s in strides)        # the library counts elements, two a byte
+            for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.uint8:
+                    raise TypeError(f"{what} must be a uint8 device (cuda/hip) tensor")
+                if t.shape != k.shape[:3] + (shape[3] // 32,):
+                    raise ValueError(f"{what} must be [n_pages, n_kv, page_size, head_dim/32]")
+            scale_strides = _view_strides(k_scale, 3, "k_scale")
+            if scale_strides != _view_strides(v_scale, 3, "v_scale"):
+                raise ValueError("k_scale and v_scale must have the same strides")
         self.device = k.device
         for t in (v,) if k_scale is None else (v, k_scale, v_scale):
             if t.device != k.device:
                 raise ValueError(f"tensors on {k.device} and {t.device}")
         self._index = k.get_device()
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.n_kv, self.page_size, self.head_dim = k.shape
+        self.n_pages, self.n_kv, self.page_size, self.head_dim = shape
         self._struct = _KvCacheStruct(
             k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
-            None if v_scale is None else v_scale.data_ptr(), *k.shape, *strides, *scale_strides, KV_KINDS[self.kind])
+            None if v_scale is None else v_scale.data_ptr(), *shape, *strides, *scale_strides, KV_KINDS[self.kind])
         self._ptr = ctypes.addressof(self._struct)
 
 
@@ -625,7 +651,8 @@ def _load_step():
     from . import _step
     _step.bind(*(ctypes.cast(getattr(lib, "qmm_" + n), ctypes.c_void_p).value
                  for n in ("paged_extend", "kv_append", "paged_attention", "paged_attention_workspace_bytes",
-                           "add_rmsnorm", "add_rmsnorm_q8")))
+                           "add_rmsnorm", "add_rmsnorm_q8", "add_rmsnorm_mxfp4", "quantize_mxfp4", "dequantize_mxfp4",
+                           "gemm_mxfp4")))
     _current_device = getattr(torch._C, "_cuda_getDevice", None)
     _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _STEP = _step
@@ -752,3 +779,63 @@ def add_rmsnorm_q8(x, weight, residual=None, eps: float = 1e-5, q=None, d=None, 
         h = _new(x.shape, x.dtype, x, stream)
     _run(step.add_rmsnorm_q8, dev, stream, x, weight, residual, eps, q, d, h)
     return q, d, h
+
+
+# ------------------------------------------------------------------ MXFP4
+def quantize_mxfp4(x, q=None, e=None, stream=None):
+    """MXFP4 codes and scales of x (float32, float16 or bfloat16 [rows, k], k a multiple of 32, rows
+    any multiple of 16 bytes apart): returns (q uint8 [rows, k/2], e uint8 [rows, k/32]).  A value is
+    code * 2^(e - 127), value 2j in the low half of byte j; the scale is 2^(floor(log2 max|x|) - 2)
+    over 32 consecutive values, codes round to nearest even."""
+    step = _STEP or _load_step()
+    dev = step.device(x, "x")
+    if q is None or e is None:
+        import torch
+        q = _new((x.shape[0], x.shape[-1] // 2), torch.uint8, x, stream) if q is None else q
+        e = _new((x.shape[0], x.shape[-1] // 32), torch.uint8, x, stream) if e is None else e
+    _run(step.quantize_mxfp4, dev, stream, x, q, e)
+    return q, e
+
+
+def dequantize_mxfp4(q, e, out=None, stream=None):
+    """The float32 values [.., k] of MXFP4 codes q (uint8 [.., k/2]) and scales e (uint8 [.., k/32]),
+    all contiguous."""
+    step = _STEP or _load_step()
+    dev = step.device(q, "q")
+    if out is None:
+        import torch
+        out = _new(tuple(q.shape[:-1]) + (2 * q.shape[-1],), torch.float32, q, stream)
+    _run(step.dequantize_mxfp4, dev, stream, q, e, out)
+    return out
+
+
+def gemm_mxfp4(wq, we, xq, xe, x_scale=None, out=None, stream=None):
+    """dst[n, m] with dst[j, i] = x_scale[j] * sum_c w[i, c] * x[j, c], both sides in MXFP4: wq, we
+    the codes [m, k/2] and scales [m, k/32] of the weights, xq, xe those of the activations [n, ..]
+    (quantize_mxfp4); x_scale: float32 [n] (add_rmsnorm_mxfp4) or None; out: optional float32 [n, m],
+    rows any stride apart.  Exact products, f32 sums."""
+    step = _STEP or _load_step()
+    dev = step.device(wq, "wq")
+    if out is None:
+        import torch
+        out = _new((xq.shape[0], wq.shape[0]), torch.float32, wq, stream)
+    _run(step.gemm_mxfp4, dev, stream, wq, we, xq, xe, x_scale, out)
+    return out
+
+
+def add_rmsnorm_mxfp4(x, weight, residual=None, eps: float = 1e-5, q=None, e=None, s=None, h=None, stream=None):
+    """add_rmsnorm with y in MXFP4, ready for gemm_mxfp4; returns (q uint8 [n, k/2], e uint8 [n, k/32],
+    s float32 [n], h): q and e are those of h * weight, s the rows' factors 1/rms (gemm_mxfp4's
+    x_scale).  k a multiple of 32."""
+    step = _STEP or _load_step()
+    dev = step.device(x, "x")
+    if q is None or e is None or s is None:
+        import torch
+        n, k = x.shape
+        q = _new((n, k // 2), torch.uint8, x, stream) if q is None else q
+        e = _new((n, k // 32), torch.uint8, x, stream) if e is None else e
+        s = _new(n, torch.float32, x, stream) if s is None else s
+    if h is None and residual is not None:
+        h = _new(x.shape, x.dtype, x, stream)
+    _run(step.add_rmsnorm_mxfp4, dev, stream, x, weight, residual, eps, q, e, s, h)
+    return q, e, s, h

@@ -25,7 +25,7 @@ STEP_OUT = os.path.join(PKG, "_step.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["gemv.hip", "moe.hip", "gemm_mfma.hip", "gemm_lds.hip", "noalloc.hip", "kv_cache.hip", "attention.hip",
-           "norm.hip", "qmm_api.cpp"]
+           "norm.hip", "mxfp4.hip", "gemm_mx.hip", "qmm_api.cpp"]
 ARCH = os.environ.get("QMM_OFFLOAD_ARCH", "gfx950")
 
 

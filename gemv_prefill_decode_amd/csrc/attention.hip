@@ -18,7 +18,9 @@
 // of two that cancel at the end; bf16 parts have f32's exponents and only stay
 // clear of its ends, keys and values reaching as far as f32's.  8-bit rows are
 // exact as f16 codes; a key's scale multiplies its score, a value's scale its
-// probability.
+// probability.  MXFP4 rows (mxfp4.hpp) become bf16 on their way into the matrix
+// cores, where a code times its block's power of two is exact, and are treated
+// as a bf16 cache from there on.
 //
 // Tiles.  A wave takes 32 tokens at a time: scores as K q^T (two 16-token
 // tiles: lane (c, i) = (lane / 16, lane % 16) gets head i's scores of tokens
@@ -48,8 +50,11 @@
 // sequences of up to 8192 8-bit tokens, 382 MB, 72 us (5.3 TB/s; vector ALUs
 // about half busy, most of it the codes' conversion); one sequence of 97 tokens,
 // heads of 64, 5.1 us (launch and four dependent loads).
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
+#include "mxfp4.hpp"
 
 namespace qmm {
 
@@ -63,7 +68,7 @@ constexpr int HEADS = 16;     // query heads per pass over a unit's rows
 // (8-bit: 64 KB) of loads in flight on a CU, and more read no faster: with
 // three or four, where the registers allow it, 8-bit heads of 128 went from
 // 103 to 121 us and f16 heads of 64 from 92 to 97 us (64 sequences of 4096).
-constexpr int occupancy(int kind, int nb) { return nb <= (kind == KV_Q8 ? 6 : 5) ? 2 : 1; }
+constexpr int occupancy(int kind, int nb) { return kind == KV_MX4 || nb <= (kind == KV_Q8 ? 6 : 5) ? 2 : 1; }
 // What a unit's start and end cost its wave, in tiles: its loads are not ahead
 // of it, and its sums are written.  Counted where a wave has at least
 // START_MIN tiles, so that the waves with many short units are not the last
@@ -140,6 +145,8 @@ __device__ __forceinline__ void ldg(uint32_t (&dst)[N], int at, const char* p, i
         dst[at] = v.x; dst[at + 1] = v.y;
     } else if (bytes == 4) {
         dst[at] = ldx<NT, uint32_t>(p);
+    } else if (bytes == 1) {
+        dst[at] = ldx<NT, uint8_t>(p);
     } else {
         dst[at] = ldx<NT, uint16_t>(p);
     }
@@ -147,15 +154,18 @@ __device__ __forceinline__ void ldg(uint32_t (&dst)[N], int at, const char* p, i
 
 // Eight f32 as f16 (bf16) parts: x = part 0 + part 1 (+ part 2) up to 2^-22
 // (2^-24) of |x|.
+// Kinds whose arithmetic is in bf16 parts.
+constexpr bool in_bf16(int kind) { return kind == KV_BF16 || kind == KV_MX4; }
+
 template <int KIND>
-__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&part)[KIND == KV_BF16 ? 3 : 2]) {
-    constexpr int NS = KIND == KV_BF16 ? 3 : 2;
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&part)[in_bf16(KIND) ? 3 : 2]) {
+    constexpr int NS = in_bf16(KIND) ? 3 : 2;
     float rest[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) rest[j] = x[j];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-        if constexpr (KIND == KV_BF16) {
+        if constexpr (in_bf16(KIND)) {
             bf16x8 v;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -177,7 +187,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&part)[KIND =
 
 template <int KIND>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-    if constexpr (KIND == KV_BF16)
+    if constexpr (in_bf16(KIND))
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -192,20 +202,49 @@ __device__ __forceinline__ uint32_t codes2(uint32_t bytes, bool high) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// The N scale bytes of an MXFP4 row, byte b in bits 8b of the pair.
+template <int N>
+__device__ __forceinline__ u32x2 scale_bytes(const uint8_t* p) {
+    uint32_t lo = 0, hi = 0;
+    if constexpr (N >= 4) __builtin_memcpy(&lo, p, 4);
+    if constexpr (N == 8) __builtin_memcpy(&hi, p + 4, 4);
+    constexpr int AT = N & 4, REST = N & 3;
+    uint32_t rest = 0;
+    if constexpr (REST >= 2) {
+        uint16_t h;
+        __builtin_memcpy(&h, p + AT, 2);
+        rest = h;
+    }
+    if constexpr (REST & 1) rest |= (uint32_t)p[AT + REST - 1] << (8 * (REST - 1));
+    if constexpr (REST > 0 && AT) hi = rest;
+    if constexpr (REST > 0 && !AT) lo = rest;
+    return u32x2{lo, hi};
+}
+// Scale of block b, 2^(byte - 127), as the scaled conversions take it.
+__device__ __forceinline__ float block_scale(u32x2 w, int b) {
+    return mx_scale(((b & 4 ? w.y : w.x) >> (8 * (b & 3))) & 255u);
+}
+// Codes 2 BYTE and 2 BYTE + 1 of a dword as bf16, exact.
+template <int BYTE>
+__device__ __forceinline__ uint32_t mx_bf16x2(uint32_t codes, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, BYTE));
+}
+
 // One wave's state over a segment (some tiles of one unit), head i = lane % 16:
 // acc[o][r] belongs to the value dimension of operand o that lane 4c + r loads.
 template <int KIND, int NB>
 struct Segment {
     static constexpr int D = 32 * NB;
-    static constexpr bool Q8 = KIND == KV_Q8;
-    static constexpr int NS = KIND == KV_BF16 ? 3 : 2;
-    static constexpr int ES = Q8 ? 1 : 2;          // bytes per element
-    static constexpr int KW = Q8 ? 2 * NB : 4 * NB;  // dwords of a lane's share of a key tile row
-    static constexpr int VW = Q8 ? (NB + 1) / 2 : NB;
+    static constexpr bool Q8 = KIND == KV_Q8, MX = KIND == KV_MX4;
+    static constexpr int NS = in_bf16(KIND) ? 3 : 2;
+    static constexpr int BITS = MX ? 4 : Q8 ? 8 : 16;  // of an element
+    static constexpr int ROW = D * BITS / 8;           // bytes of a row
+    static constexpr int KW = ROW / 16;                // dwords of a lane's share of a key tile row
     // A value row is read by 16 lanes in runs of 8 elements per lane (128
     // dimensions), then 4 (64) and 2 (32) as head_dim leaves them.
     static constexpr int N8 = NB / 4;
     static constexpr bool N4 = (NB & 2) != 0, N2 = (NB & 1) != 0;
+    static constexpr int VW = MX ? N8 + N4 + N2 : Q8 ? (NB + 1) / 2 : NB;
 
     f32x4 acc[2 * NB];
     float m, l;
@@ -218,11 +257,12 @@ struct Segment {
     // Rows of whole lines are read once and past the caches (non-temporal: 131071
     // tokens of f16 heads of 128 94.9 -> 91.1 us); rows that share lines are not
     // (2048 tokens x 64 of 8-bit heads of 96: 63 us, non-temporal 84).
-    static constexpr bool STREAM = D * ES % 128 == 0;
+    static constexpr bool STREAM = ROW % 128 == 0;
 
-    // A key row's 128-byte lines, then what is left: 64 and 32 bytes.
-    static constexpr int LINES = D * ES / 128;
-    static constexpr bool REST64 = (D * ES & 64) != 0, REST32 = (D * ES & 32) != 0;
+    // A key row's 128-byte lines, then what is left: 64, 32 and 16 bytes.
+    static constexpr int LINES = ROW / 128;
+    static constexpr bool REST64 = (ROW & 64) != 0, REST32 = (ROW & 32) != 0, REST16 = (ROW & 16) != 0;
+    static constexpr int AT32 = 128 * LINES + 64 * REST64, AT16 = AT32 + 32 * REST32;  // where they begin
 
     // The lane's share of 16 rows: row i (its operand row), which needs the
     // 16-byte chunks 2c and 2c + 1 of every line.  A load instruction takes
@@ -238,7 +278,8 @@ struct Segment {
             ldg<STREAM>(kr, 8 * n + 4, odd + at, 16);
         }
         if constexpr (REST64) ldg<STREAM>(kr, 8 * LINES, own + 128 * LINES + 16 * c, 16);
-        if constexpr (REST32) ldg<STREAM>(kr, 8 * LINES + (REST64 ? 4 : 0), own + D * ES - 32 + 8 * c, 8);
+        if constexpr (REST32) ldg<STREAM>(kr, AT32 / 16, own + AT32 + 8 * c, 8);
+        if constexpr (REST16) ldg<STREAM>(kr, AT16 / 16, own + AT16 + 4 * c, 4);
     }
     static __device__ __forceinline__ void settle(uint32_t (&kr)[KW], int i) {
         const bool odd = i & 1;
@@ -255,6 +296,14 @@ struct Segment {
             }
     }
     static __device__ __forceinline__ void load_v(uint32_t (&vr)[VW], const char* row, int i) {
+        if constexpr (MX) {
+#pragma unroll
+            for (int n = 0; n < N8; ++n) ldg<STREAM>(vr, n, row + 64 * n + 4 * i, 4);
+            if constexpr (N4) ldg<STREAM>(vr, N8, row + 64 * N8 + 2 * i, 2);
+            if constexpr (N2) ldg<STREAM>(vr, N8 + N4, row + 64 * N8 + 32 * N4 + i, 1);
+            return;
+        }
+        constexpr int ES = BITS / 8;
 #pragma unroll
         for (int n = 0; n < N8; ++n) ldg<STREAM>(vr, n * 2 * ES, row + ES * (128 * n + 8 * i), 8 * ES);
         if constexpr (N4) ldg<STREAM>(vr, N8 * 2 * ES, row + ES * (128 * N8 + 4 * i), 4 * ES);
@@ -262,15 +311,21 @@ struct Segment {
     }
     // first dimension of the eight that lane c's share of step s holds
     static __device__ __forceinline__ int kdim(int s, int c) {
-        constexpr int CH = 16 / ES, PER = 32 / ES / 8;  // dimensions in a chunk; steps of a line
-        if (s < PER * LINES) return 128 / ES * (s / PER) + 2 * CH * c + 8 * (s % PER);
+        constexpr int CH = 128 / BITS, PER = CH / 4;  // dimensions in a chunk; steps of a line
+        if (s < PER * LINES) return 8 * CH * (s / PER) + 2 * CH * c + 8 * (s % PER);
         s -= PER * LINES;
-        if (REST64 && s < PER / 2) return 128 / ES * LINES + CH * c + 8 * s;
-        return D - 32 + 8 * c;  // 32 bytes: 8-bit rows
+        if (REST64 && s < PER / 2) return 8 * CH * LINES + CH * c + 8 * s;
+        if (REST64) s -= PER / 2;
+        // 32 bytes: 8-bit rows, MXFP4 rows (two steps); 16: MXFP4 rows
+        if (REST32 && s < PER / 4) return AT32 * 8 / BITS + CH / 2 * c + 8 * s;
+        return D - 32 + 8 * c;
     }
-    // the key operand of step s
-    static __device__ __forceinline__ u32x4 key(const uint32_t (&kr)[KW], int s) {
-        if constexpr (Q8) {
+    // the key operand of step s; MXFP4: with the scale of its block
+    static __device__ __forceinline__ u32x4 key(const uint32_t (&kr)[KW], int s, float scale = 1.0f) {
+        if constexpr (MX) {
+            return u32x4{mx_bf16x2<0>(kr[s], scale), mx_bf16x2<1>(kr[s], scale), mx_bf16x2<2>(kr[s], scale),
+                         mx_bf16x2<3>(kr[s], scale)};
+        } else if constexpr (Q8) {
             const uint32_t x = kr[2 * s] ^ SIGNS, y = kr[2 * s + 1] ^ SIGNS;
             return u32x4{codes2(x, false), codes2(x, true), codes2(y, false), codes2(y, true)};
         } else {
@@ -297,6 +352,18 @@ struct Segment {
         return u32x4{out[0], out[1], out[2], out[3]};
     }
 
+    // MXFP4: the value operands o and o + 1 (o even), from dword w of the rows, its byte BYTE
+    template <int BYTE>
+    static __device__ __forceinline__ void value2(const uint32_t (&vr)[8][VW], int w, const float (&scale)[8], u32x4* lo,
+                                                  u32x4* hi) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a = mx_bf16x2<BYTE>(vr[2 * j][w], scale[2 * j]), b = mx_bf16x2<BYTE>(vr[2 * j + 1][w], scale[2 * j + 1]);
+            (*lo)[j] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            (*hi)[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        }
+    }
+
     // Tiles [t, t + n) of sequence b (len tokens) for `rows` heads from query head head0.
     __device__ __forceinline__ void run(const AttnArgs& a, int b, int len, int kvh, int head0, int rows, int t, int n) {
         const int lane = threadIdx.x & 63, c = lane >> 4, i = lane & 15;
@@ -313,9 +380,10 @@ struct Segment {
         const char* kb = (const char*)a.k + (int64_t)kvh * a.head_bytes;
         const char* vb = (const char*)a.v + (int64_t)kvh * a.head_bytes;
         const float* sb = Q8 ? ((lane & 32) ? a.v_scale : a.k_scale) + (int64_t)kvh * a.scale_head : nullptr;
+        const uint8_t* mb = MX ? (const uint8_t*)((lane & 32) ? a.v_scale : a.k_scale) + (int64_t)kvh * a.scale_head : nullptr;
         const int* table = a.table + (int64_t)b * a.table_stride;
         bool bad = false;
-        const float pbits = KIND == KV_BF16 ? (float)-log2_up(len) : Q8 ? 0.0f : PBITS;
+        const float pbits = in_bf16(KIND) ? (float)-log2_up(len) : Q8 ? 0.0f : PBITS;
 
         // page id of the lane's token (lane % 32) of tile tt; tokens behind the last read as the last
         auto token = [&](int tt) {
@@ -325,12 +393,14 @@ struct Segment {
         auto page_id = [&](int tt) { return table[token(tt) >> a.page_log2]; };
         uint32_t off;        // the row of the lane's token, in 16-byte units from the head's first
         float sc = 0.0f;     // its key (lanes 0..31) or value scale
+        u32x2 mx = {0, 0};   // MXFP4: its blocks' scales
         auto locate = [&](int id, int tt) {
             const bool out = (uint32_t)id >= (uint32_t)a.n_pages;
             bad |= out;
             const uint32_t pg = out ? 0u : (uint32_t)id, slot = (uint32_t)token(tt) & (uint32_t)(a.page_size - 1);
             off = pg * a.page_units + slot * a.slot_units;
             if constexpr (Q8) sc = sb[(int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot];
+            if constexpr (MX) mx = scale_bytes<NB>(mb + (int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot);
         };
         auto row_of = [&](const char* base, int src) {
             return base + ((uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(4 * src, (int)off) << 4);
@@ -340,7 +410,13 @@ struct Segment {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 load_k(kr[h], row_of(kb, 16 * h + (i & ~1)), row_of(kb, 16 * h + (i | 1)),
-                       REST64 || REST32 ? row_of(kb, 16 * h + i) : kb, c, i);
+                       REST64 || REST32 || REST16 ? row_of(kb, 16 * h + i) : kb, c, i);
+        };
+        // the scales of the token that lane src located
+        auto scales_of = [&](int src) {
+            u32x2 w = {(uint32_t)__builtin_amdgcn_ds_bpermute(4 * src, (int)mx.x), 0};
+            if constexpr (NB > 4) w.y = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * src, (int)mx.y);
+            return w;
         };
         auto tok_of = [&](int j) { return (j < 4 ? 0 : 12) + 4 * c + j; };  // token of the lane's k index j
         auto load_values = [&]() {
@@ -373,7 +449,7 @@ struct Segment {
             top = max_c(top);
             // q's factor, a power of two: its exponent field
             int e;
-            if constexpr (KIND == KV_BF16) {
+            if constexpr (in_bf16(KIND)) {
                 // 2^-12, so that the sum of products passes f32 no sooner than the score, but at
                 // least what takes the largest to 2^-60: its parts are normal numbers
                 e = 194 - (int)(ubits(top) >> 23);
@@ -399,12 +475,30 @@ struct Segment {
             f32x4 s4[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
             settle(kr[0], i);
             settle(kr[1], i);
+            if constexpr (MX) {
 #pragma unroll
-            for (int s = 0; s < NB; ++s)
+                for (int h = 0; h < 2; ++h) {
+                    const u32x2 w = scales_of(16 * h + i);
 #pragma unroll
-                for (int p = 0; p < NS; ++p)
+                    for (int s = 0; s < NB; ++s) {
+                        const u32x4 k = key(kr[h], s, block_scale(w, kdim(s, c) / 32));
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) s4[h] = mfma<KIND>(key(kr[h], s), qp[s][p], s4[h]);
+                        for (int p = 0; p < NS; ++p) s4[h] = mfma<KIND>(k, qp[s][p], s4[h]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < NB; ++s)
+#pragma unroll
+                    for (int p = 0; p < NS; ++p)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) s4[h] = mfma<KIND>(key(kr[h], s), qp[s][p], s4[h]);
+            }
+            u32x2 vmx[8];  // MXFP4: the scales of the lane's eight value rows
+            if constexpr (MX) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) vmx[j] = scales_of(32 + tok_of(j));
+            }
             float s[8], vs[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -471,11 +565,39 @@ struct Segment {
             }
             u32x4 pp[NS];
             split8<KIND>(p, pp);
+            if constexpr (MX) {
+                // dword w of the value rows: N of its bytes, two operands each, from operand o on, of block b
+                auto dword = [&](auto n, int w, int o, int b) {
+                    float scale[8];
 #pragma unroll
-            for (int o = 0; o < 2 * NB; ++o) {
-                const u32x4 v = value(vr, o);
+                    for (int j = 0; j < 8; ++j) scale[j] = block_scale(vmx[j], b);
+                    auto byte = [&](auto at) {
+                        u32x4 lo, hi;
+                        value2<at>(vr, w, scale, &lo, &hi);
 #pragma unroll
-                for (int q = 0; q < NS; ++q) acc[o] = mfma<KIND>(v, pp[q], acc[o]);
+                        for (int q = 0; q < NS; ++q) {
+                            acc[o + 2 * at] = mfma<KIND>(lo, pp[q], acc[o + 2 * at]);
+                            acc[o + 2 * at + 1] = mfma<KIND>(hi, pp[q], acc[o + 2 * at + 1]);
+                        }
+                    };
+                    byte(std::integral_constant<int, 0>{});
+                    if constexpr (n > 1) byte(std::integral_constant<int, 1>{});
+                    if constexpr (n > 2) {
+                        byte(std::integral_constant<int, 2>{});
+                        byte(std::integral_constant<int, 3>{});
+                    }
+                };
+#pragma unroll
+                for (int n = 0; n < N8; ++n) dword(std::integral_constant<int, 4>{}, n, 8 * n, 4 * n + i / 4);
+                if constexpr (N4) dword(std::integral_constant<int, 2>{}, N8, 8 * N8, 4 * N8 + i / 8);
+                if constexpr (N2) dword(std::integral_constant<int, 1>{}, N8 + N4, 2 * NB - 2, NB - 1);
+            } else {
+#pragma unroll
+                for (int o = 0; o < 2 * NB; ++o) {
+                    const u32x4 v = value(vr, o);
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) acc[o] = mfma<KIND>(v, pp[q], acc[o]);
+                }
             }
             if (more) load_values();
         }
@@ -900,6 +1022,8 @@ void launch_paged_attention(const AttnArgs& a, int head_dim, hipStream_t st) {
         launch_kind<KV_F16>(a, head_dim, st);
     else if (a.kind == KV_BF16)
         launch_kind<KV_BF16>(a, head_dim, st);
+    else if (a.kind == KV_MX4)
+        launch_kind<KV_MX4>(a, head_dim, st);
     else
         launch_kind<KV_Q8>(a, head_dim, st);
 }

@@ -1,6 +1,7 @@
 // The paged key-value cache's bookkeeping and its writer.
 #include "common.hpp"
 #include "kernels.hpp"
+#include "mxfp4.hpp"
 
 namespace qmm {
 
@@ -186,6 +187,15 @@ __global__ __launch_bounds__(APP_THREADS) void kv_append_kernel(const AppendArgs
                 if (e == 0)
                     (second ? a.vs : a.ks)[page * a.scale_page + head * a.scale_head + in_page * a.scale_slot] = d;
             }
+        } else if constexpr (KIND == KV_MX4) {
+            const uint32_t byte = mx_scale_byte(mx_quad_max(mx_max8(lo, hi)));  // a quad of lanes holds a block
+            const uint32_t codes = mx_codes8(lo, hi, byte);
+            if (live) {
+                *(uint32_t*)((uint8_t*)(second ? a.vc : a.kc) + at / 2) = codes;
+                if ((e & 3) == 0)
+                    ((uint8_t*)(second ? a.vs : a.ks))[page * a.scale_page + head * a.scale_head + in_page * a.scale_slot +
+                                                       e / 4] = (uint8_t)byte;
+            }
         } else if (live) {
             u32x4 w;
 #pragma unroll
@@ -246,6 +256,8 @@ void launch_kv_append(const AppendArgs& a, int kind, int head_dim, hipStream_t s
         append_kind<KV_F16>(a, head_dim, st);
     else if (kind == KV_BF16)
         append_kind<KV_BF16>(a, head_dim, st);
+    else if (kind == KV_MX4)
+        append_kind<KV_MX4>(a, head_dim, st);
     else
         append_kind<KV_Q8>(a, head_dim, st);
 }

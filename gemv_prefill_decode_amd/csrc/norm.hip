@@ -1,4 +1,4 @@
-// RMS norm with the residual's addition, to f32 or to Q8_1 activations.
+// RMS norm with the residual's addition, to f32, Q8_1 or MXFP4 activations.
 //
 //     h = x + r,  y = h * w / sqrt(mean(h^2) + eps)
 //
@@ -11,10 +11,14 @@
 // those of z = h * w, d0 = max|z| / 127, q = round(z * (1/d0)) (halves away
 // from zero, every step in f32 as qmm_quantize_q8_1), and its scale is d0/rms:
 // the codes do not depend on the order in which the squares were added.
+//
+// MXFP4 output (mxfp4.hpp) the same way: its scales are powers of two and cannot
+// take 1/rms, which is written once per row for the product to multiply by.
 #include <type_traits>
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "mxfp4.hpp"
 
 namespace qmm {
 
@@ -49,6 +53,18 @@ __device__ __forceinline__ uint32_t codes4(f32x4 z, float* d0) {
     return bits < 0x7f800000u ? codes : 0;
 }
 
+// The MXFP4 codes of a block held by eight consecutive lanes, four values each.
+__device__ __forceinline__ uint32_t mx_codes_of(f32x4 z, uint32_t* byte) {
+    uint32_t bits = mx_larger(mx_larger(mx_magnitude(z.x), mx_magnitude(z.y)), mx_larger(mx_magnitude(z.z), mx_magnitude(z.w)));
+    bits = mx_quad_max(bits);
+    bits = mx_larger(bits, (uint32_t)__shfl_xor((int)bits, 4));
+    *byte = mx_scale_byte(bits);
+    return mx_codes4(z, *byte);
+}
+
+// What y is written as.
+enum : int { TO_F32 = 0, TO_Q8 = 1, TO_MX = 2 };
+
 template <bool NT>
 __device__ __forceinline__ f32x4 ld(const f32x4* p) {
     return NT ? __builtin_nontemporal_load(p) : *p;
@@ -57,8 +73,8 @@ __device__ __forceinline__ f32x4 ld(const f32x4* p) {
 // THREADS threads per work group, T of them per row, V float4 per thread: a
 // row of up to 4*T*V elements.  NT: rows read past the caches.  LOOP: longer
 // rows, read a second time.
-template <int THREADS, int T, int V, bool Q8, bool NT, bool LOOP>
-__global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(const NormArgs a) {
+template <int THREADS, int T, int V, int OUT, bool NT, bool LOOP, typename Args>
+__global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(const Args a) {
     constexpr int ROWS = THREADS / T;
     __shared__ float wave_sum[THREADS / 64];
     const int tid = threadIdx.x, at = tid % T, nv = a.k / 4;
@@ -97,6 +113,8 @@ __global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(const NormArgs a) 
         for (int i = 0; i < THREADS / 64; ++i) sum += wave_sum[i];
     }
     const float inv = 1.0f / sqrtf(sum * a.inv_k + a.eps);
+    if constexpr (OUT == TO_MX)
+        if (live && at == 0) a.d[row] = inv;
     for (int base = 0; base < span; base += T * V) {
         if constexpr (LOOP) {
 #pragma unroll
@@ -110,7 +128,14 @@ __global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(const NormArgs a) 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = base + i * T + at;
-            if constexpr (Q8) {
+            if constexpr (OUT == TO_MX) {
+                uint32_t byte;
+                const uint32_t c = mx_codes_of(h[i] * wt[i], &byte);
+                if (live && e < nv) {
+                    ((uint16_t*)a.q)[row * nv + e] = (uint16_t)c;
+                    if ((e & 7) == 0) a.e[(row * nv + e) / 8] = (uint8_t)byte;
+                }
+            } else if constexpr (OUT == TO_Q8) {
                 float d0;
                 const uint32_t c = codes4(h[i] * wt[i], &d0);
                 if (live && e < nv) {
@@ -124,8 +149,9 @@ __global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(const NormArgs a) 
     }
 }
 
-template <int THREADS, int T, int V, bool LOOP = false>
-void launch(const NormArgs& all, hipStream_t st) {
+template <int THREADS, int T, int V, bool LOOP = false, typename Args>
+void launch(const Args& all, hipStream_t st) {
+    constexpr bool MX = std::is_same_v<Args, NormMxArgs>;
     constexpr int ROWS = THREADS / T;
     // Large inputs are read past the caches.  Kernel times so (and through them)
     // with x and the residual just written, with x just written, and with neither,
@@ -138,31 +164,40 @@ void launch(const NormArgs& all, hipStream_t st) {
     // a launch has fewer than 2^32 threads
     constexpr int64_t MOST = ((int64_t)1 << 31) / THREADS * ROWS;
     for (int64_t first = 0; first < all.n; first += MOST) {
-        NormArgs a = all;
+        Args a = all;
         a.n = all.n - first < MOST ? all.n - first : MOST;
         a.x += first * a.x_stride;
         if (a.r) a.r += first * a.r_stride;
         if (a.h) a.h += first * a.h_stride;
         if (a.y) a.y += first * a.y_stride;
-        if (a.q) {
-            a.q += first * a.k;
-            a.d += first * (a.k / 32);
-        }
         const dim3 grid((unsigned)((a.n + ROWS - 1) / ROWS));
-        if (a.q && nt)
-            add_rmsnorm_kernel<THREADS, T, V, true, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
-        else if (a.q)
-            add_rmsnorm_kernel<THREADS, T, V, true, false, LOOP><<<grid, THREADS, 0, st>>>(a);
-        else if (nt)
-            add_rmsnorm_kernel<THREADS, T, V, false, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
-        else
-            add_rmsnorm_kernel<THREADS, T, V, false, false, LOOP><<<grid, THREADS, 0, st>>>(a);
+        if constexpr (MX) {
+            a.q += first * (a.k / 2);
+            a.e += first * (a.k / 32);
+            a.d += first;
+            if (nt)
+                add_rmsnorm_kernel<THREADS, T, V, TO_MX, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
+            else
+                add_rmsnorm_kernel<THREADS, T, V, TO_MX, false, LOOP><<<grid, THREADS, 0, st>>>(a);
+        } else {
+            if (a.q) {
+                a.q += first * a.k;
+                a.d += first * (a.k / 32);
+            }
+            if (a.q && nt)
+                add_rmsnorm_kernel<THREADS, T, V, TO_Q8, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
+            else if (a.q)
+                add_rmsnorm_kernel<THREADS, T, V, TO_Q8, false, LOOP><<<grid, THREADS, 0, st>>>(a);
+            else if (nt)
+                add_rmsnorm_kernel<THREADS, T, V, TO_F32, !LOOP, LOOP><<<grid, THREADS, 0, st>>>(a);
+            else
+                add_rmsnorm_kernel<THREADS, T, V, TO_F32, false, LOOP><<<grid, THREADS, 0, st>>>(a);
+        }
     }
 }
 
-}  // namespace
-
-void launch_add_rmsnorm(const NormArgs& a, int num_cu, hipStream_t st) {
+template <typename Args>
+void launch_norm(const Args& a, int num_cu, hipStream_t st) {
     const int nv = a.k / 4;
     if (nv <= 8) return launch<256, 8, 1>(a, st);
     if (nv <= 16) return launch<256, 16, 1>(a, st);
@@ -184,5 +219,10 @@ void launch_add_rmsnorm(const NormArgs& a, int num_cu, hipStream_t st) {
     if (nv <= 4096) return launch<1024, 1024, 4>(a, st);
     launch<1024, 1024, 4, true>(a, st);
 }
+
+}  // namespace
+
+void launch_add_rmsnorm(const NormArgs& a, int num_cu, hipStream_t st) { launch_norm(a, num_cu, st); }
+void launch_add_rmsnorm_mxfp4(const NormMxArgs& a, int num_cu, hipStream_t st) { launch_norm(a, num_cu, st); }
 
 }  // namespace qmm

@@ -14,6 +14,7 @@
 #include <mutex>
 
 #include "kernels.hpp"
+#include "mxfp4.hpp"
 
 namespace {
 
@@ -317,6 +318,10 @@ int gemm_impl(float* dst, int64_t ldd, const void* w, const float* x, int64_t ld
     return launch_status();
 }
 
+// Largest sizes of an MXFP4 product: 256 rows of k/2 bytes below 2^31, 2^20
+// tokens.
+constexpr int64_t MX_K_MAX = (int64_t)1 << 23, MX_N_MAX = (int64_t)1 << 20;
+
 // ------------------------------------------------------------------ decode step
 // Tokens of a cache or a table row, table entries and rows of a step: int32
 // with room for the kernels' strides and tiles past the last.
@@ -372,17 +377,23 @@ bool holds_end(const void* a, int64_t bytes, const void* b, int64_t b_bytes, int
     return overlap(a, bytes, b, row) || overlap(a, bytes, (const char*)b + (b_bytes - row), row);
 }
 
+// Bytes of n elements of a cache (MXFP4: n even).
+int64_t kv_bytes(const qmm_kv_cache* c, int64_t n) {
+    return c->kind == QMM_KV_MXFP4 ? n / 2 : c->kind == QMM_KV_Q8 ? n : 2 * n;
+}
+
 int check_cache(const qmm_kv_cache* c, KvExtent* e) {
     if (!c || !c->k || !c->v) return QMM_ERR_NULL;
-    if (c->kind != QMM_KV_F16 && c->kind != QMM_KV_BF16 && c->kind != QMM_KV_Q8) return QMM_ERR_QTYPE;
-    const bool q8 = c->kind == QMM_KV_Q8;
-    if (q8 && (!c->k_scale || !c->v_scale)) return QMM_ERR_NULL;
+    if (c->kind != QMM_KV_F16 && c->kind != QMM_KV_BF16 && c->kind != QMM_KV_Q8 && c->kind != QMM_KV_MXFP4)
+        return QMM_ERR_QTYPE;
+    const bool q8 = c->kind == QMM_KV_Q8, mx = c->kind == QMM_KV_MXFP4;
+    if ((q8 || mx) && (!c->k_scale || !c->v_scale)) return QMM_ERR_NULL;
     if (c->n_pages < 1 || c->n_kv < 1 || c->page_size < 1 || c->head_dim < 1 ||
         (c->page_size & (c->page_size - 1)) != 0)
         return QMM_ERR_SHAPE;
     if (c->head_dim % 32 != 0) return QMM_ERR_K_ALIGN;
     if (c->head_dim > 256) return QMM_ERR_RANGE;
-    const int64_t unit = q8 ? 16 : 8;  // elements in 16 bytes
+    const int64_t unit = mx ? 32 : q8 ? 16 : 8;  // elements in 16 bytes
     for (const int64_t s : {c->page_stride, c->head_stride, c->slot_stride}) {
         if (s < c->head_dim) return QMM_ERR_SHAPE;
         if (s % unit != 0) return QMM_ERR_ALIGN;
@@ -393,20 +404,23 @@ int check_cache(const qmm_kv_cache* c, KvExtent* e) {
     const int64_t elems = strided_extent(c, c->page_stride, c->head_stride, c->slot_stride, c->head_dim);
     // rows are addressed by a 32-bit count of 16-byte units from a head's first row
     if (elems < 0 || elems / unit >= ((int64_t)1 << 32)) return QMM_ERR_RANGE;
-    const int64_t es = q8 ? 1 : 2;
-    e->bytes = elems * es;
+    const int64_t row = kv_bytes(c, c->head_dim);
+    e->bytes = kv_bytes(c, elems);
     e->scale_bytes = 0;
-    if (arrays_meet(c->k, c->v, e->bytes, c->head_dim * es, es,
-                    {{c->page_stride, c->n_pages}, {c->head_stride, c->n_kv}, {c->slot_stride, c->page_size}}))
+    // (a stride past int64 / 4 belongs to an axis of one entry, which arrays_meet drops)
+    auto axis = [&](int64_t s, int64_t n) { return Axis{n > 1 ? kv_bytes(c, s) : 0, n}; };
+    if (arrays_meet(c->k, c->v, e->bytes, row, 1,
+                    {axis(c->page_stride, c->n_pages), axis(c->head_stride, c->n_kv), axis(c->slot_stride, c->page_size)}))
         return QMM_ERR_ALIAS;
-    if (q8) {
+    if (q8 || mx) {
+        const int64_t per = mx ? c->head_dim / 32 : 1, ss = mx ? 1 : 4;  // scales of a row, bytes of a scale
         for (const int64_t s : {c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride})
-            if (s < 1) return QMM_ERR_SHAPE;
-        if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return QMM_ERR_ALIGN;
-        const int64_t sc = strided_extent(c, c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride, 1);
+            if (s < per) return QMM_ERR_SHAPE;
+        if (!aligned(c->k_scale, ss) || !aligned(c->v_scale, ss)) return QMM_ERR_ALIGN;
+        const int64_t sc = strided_extent(c, c->scale_page_stride, c->scale_head_stride, c->scale_slot_stride, per);
         if (sc < 0 || sc >= ((int64_t)1 << 40)) return QMM_ERR_RANGE;
-        e->scale_bytes = sc * 4;
-        if (arrays_meet(c->k_scale, c->v_scale, e->scale_bytes, 4, 4,
+        e->scale_bytes = sc * ss;
+        if (arrays_meet(c->k_scale, c->v_scale, e->scale_bytes, per * ss, ss,
                         {{c->scale_page_stride, c->n_pages}, {c->scale_head_stride, c->n_kv},
                          {c->scale_slot_stride, c->page_size}}))
             return QMM_ERR_ALIAS;
@@ -415,8 +429,8 @@ int check_cache(const qmm_kv_cache* c, KvExtent* e) {
         const int64_t rows = tokens * c->n_kv;
         for (const void* codes : {c->k, c->v})
             for (const void* scales : {c->k_scale, c->v_scale})
-                if ((elems == rows * c->head_dim && holds_end(codes, e->bytes, scales, e->scale_bytes, 4)) ||
-                    (sc == rows && holds_end(scales, e->scale_bytes, codes, e->bytes, c->head_dim)))
+                if ((elems == rows * c->head_dim && holds_end(codes, e->bytes, scales, e->scale_bytes, per * ss)) ||
+                    (sc == rows * per && holds_end(scales, e->scale_bytes, codes, e->bytes, row)))
                     return QMM_ERR_ALIAS;
     }
     return QMM_OK;
@@ -963,7 +977,6 @@ int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int
     if (overlaps_any(so.p, so.n, {sq, st_, sl, sk, sv, sks, svs, se}) ||
         overlaps_any(se.p, se.n, {sq, st_, sl, sk, sv, sks, svs}))
         return QMM_ERR_ALIAS;
-    const int64_t es = cache->kind == QMM_KV_Q8 ? 1 : 2;
     qmm::AttnArgs a{};
     a.out = out;
     a.lse = lse;
@@ -974,9 +987,9 @@ int qmm_paged_attention(float* out, int64_t ldo, float* lse, const float* q, int
     a.v = cache->v;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
-    a.head_bytes = cache->head_stride * es;
-    a.page_units = (uint32_t)(cache->page_stride * es / 16);
-    a.slot_units = (uint32_t)(cache->slot_stride * es / 16);
+    a.head_bytes = kv_bytes(cache, cache->head_stride);
+    a.page_units = (uint32_t)(kv_bytes(cache, cache->page_stride) / 16);
+    a.slot_units = (uint32_t)(kv_bytes(cache, cache->slot_stride) / 16);
     a.scale_page = cache->scale_page_stride;
     a.scale_head = cache->scale_head_stride;
     a.scale_slot = cache->scale_slot_stride;
@@ -1029,6 +1042,76 @@ int qmm_add_rmsnorm_q8(int8_t* q, float* d, float* h, int64_t ldh, const float* 
     const int st = norm_args(&a, h, ldh, x, ldx, residual, ldr, weight, n, k, eps, 32, 0);
     if (st) return st;
     qmm::launch_add_rmsnorm(a, dev_props().cu, stream);
+    return launch_status();
+}
+
+int qmm_add_rmsnorm_mxfp4(uint8_t* q, uint8_t* e, float* s, float* h, int64_t ldh, const float* x, int64_t ldx,
+                          const float* residual, int64_t ldr, const float* weight, int64_t n, int64_t k, float eps,
+                          hipStream_t stream) {
+    if (!q || !e || !s) return QMM_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(s, 4)) return QMM_ERR_ALIGN;
+    qmm::NormMxArgs a{};
+    const int st = norm_args(&a, h, ldh, x, ldx, residual, ldr, weight, n, k, eps, 32, 0);
+    if (st) return st;
+    const Span outs[] = {{q, n * k / 2}, {e, n * k / 32}, {s, n * 4}, {h, h ? ((n - 1) * ldh + k) * 4 : 0}};
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps_any(outs[i].p, outs[i].n, {{x, ((n - 1) * ldx + k) * 4}, {weight, k * 4},
+                                                {residual, residual ? ((n - 1) * ldr + k) * 4 : 0}}))
+            return QMM_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return QMM_ERR_ALIAS;
+    }
+    a.q = (int8_t*)q;
+    a.e = e;
+    a.d = s;
+    qmm::launch_add_rmsnorm_mxfp4(a, dev_props().cu, stream);
+    return launch_status();
+}
+
+int qmm_quantize_mxfp4(uint8_t* q, uint8_t* e, const void* x, int type, int64_t ldx, int64_t rows, int64_t k,
+                       hipStream_t stream) {
+    if (!q || !e || !x) return QMM_ERR_NULL;
+    if (type != QMM_MX_F32 && type != QMM_MX_F16 && type != QMM_MX_BF16) return QMM_ERR_QTYPE;
+    if (rows < 1 || k < 1 || ldx < k) return QMM_ERR_SHAPE;
+    if (k % 32 != 0) return QMM_ERR_K_ALIGN;
+    const int64_t es = type == QMM_MX_F32 ? 4 : 2;
+    if (!aligned(q, 16) || !aligned(x, 16) || ldx % (16 / es) != 0) return QMM_ERR_ALIGN;
+    int64_t span;
+    if (!mul_ok(rows, ldx, &span) || span > INT64_MAX / 4) return QMM_ERR_SHAPE;
+    if (k > INT_MAX) return QMM_ERR_RANGE;
+    const int64_t xb = ((rows - 1) * ldx + k) * es, qb = rows * k / 2, eb = rows * k / 32;
+    if (overlap(q, qb, e, eb) || overlap(q, qb, x, xb) || overlap(e, eb, x, xb)) return QMM_ERR_ALIAS;
+    qmm::launch_quantize_mxfp4(q, e, x, type, ldx, rows, k, stream);
+    return launch_status();
+}
+
+int qmm_dequantize_mxfp4(float* x, const uint8_t* q, const uint8_t* e, int64_t rows, int64_t k, hipStream_t stream) {
+    if (!x || !q || !e) return QMM_ERR_NULL;
+    if (rows < 1 || k < 1) return QMM_ERR_SHAPE;
+    if (k % 32 != 0) return QMM_ERR_K_ALIGN;
+    if (!aligned(q, 16) || !aligned(x, 16)) return QMM_ERR_ALIGN;
+    int64_t n;
+    if (!mul_ok(rows, k, &n) || n > INT64_MAX / 4) return QMM_ERR_SHAPE;
+    if (overlaps_any(x, n * 4, {{q, n / 2}, {e, n / 32}})) return QMM_ERR_ALIAS;
+    qmm::launch_dequantize_mxfp4(x, q, e, n, stream);
+    return launch_status();
+}
+
+int qmm_gemm_mxfp4(float* dst, int64_t ldd, const uint8_t* wq, const uint8_t* we, const uint8_t* xq, const uint8_t* xe,
+                   const float* x_scale, int64_t m, int64_t k, int64_t n, hipStream_t stream) {
+    if (!dst || !wq || !we || !xq || !xe) return QMM_ERR_NULL;
+    if (m < 1 || n < 1 || k < 1 || ldd < m) return QMM_ERR_SHAPE;
+    if (k % 32 != 0) return QMM_ERR_K_ALIGN;
+    if (!aligned(wq, 16) || !aligned(xq, 16) || !aligned(we, 4) || !aligned(xe, 4) || !aligned(dst, 4) || !aligned(x_scale, 4))
+        return QMM_ERR_ALIGN;
+    // a tile's rows are addressed by 31-bit byte offsets, its tokens by a grid's second axis
+    if (k > MX_K_MAX || m > INT_MAX - 256 || n > MX_N_MAX) return QMM_ERR_RANGE;
+    int64_t span;
+    if (!mul_ok(n, ldd, &span) || span > INT64_MAX / 4) return QMM_ERR_SHAPE;
+    const Span ins[] = {{wq, m * k / 2}, {we, m * k / 32}, {xq, n * k / 2}, {xe, n * k / 32}, {x_scale, x_scale ? n * 4 : 0}};
+    if (overlaps_any(dst, ((n - 1) * ldd + m) * 4, {ins[0], ins[1], ins[2], ins[3], ins[4]})) return QMM_ERR_ALIAS;
+    const qmm::MxGemmArgs a{dst, wq, we, xq, xe, x_scale, ldd, (int)m, (int)n, (int)k};
+    qmm::launch_gemm_mxfp4(a, dev_props().cu, stream);
     return launch_status();
 }
 

@@ -15,6 +15,7 @@
 #include <cmath>
 #include <cstdint>
 #include <string>
+#include <vector>
 
 #include "qmm.h"
 
@@ -26,6 +27,10 @@ decltype(&qmm_paged_attention) p_attention;
 decltype(&qmm_paged_attention_workspace_bytes) p_workspace;
 decltype(&qmm_add_rmsnorm) p_norm;
 decltype(&qmm_add_rmsnorm_q8) p_norm_q8;
+decltype(&qmm_add_rmsnorm_mxfp4) p_norm_mx;
+decltype(&qmm_quantize_mxfp4) p_quantize_mx;
+decltype(&qmm_dequantize_mxfp4) p_dequantize_mx;
+decltype(&qmm_gemm_mxfp4) p_gemm_mx;
 
 struct Refused {};  // a Python exception is set
 
@@ -154,6 +159,10 @@ int64_t bind(PyObject* const* a) {
     p_workspace = (decltype(p_workspace))(uintptr_t)integer(a[3]);
     p_norm = (decltype(p_norm))(uintptr_t)integer(a[4]);
     p_norm_q8 = (decltype(p_norm_q8))(uintptr_t)integer(a[5]);
+    p_norm_mx = (decltype(p_norm_mx))(uintptr_t)integer(a[6]);
+    p_quantize_mx = (decltype(p_quantize_mx))(uintptr_t)integer(a[7]);
+    p_dequantize_mx = (decltype(p_dequantize_mx))(uintptr_t)integer(a[8]);
+    p_gemm_mx = (decltype(p_gemm_mx))(uintptr_t)integer(a[9]);
     return 0;
 }
 
@@ -250,17 +259,92 @@ int64_t add_rmsnorm_q8(PyObject* const* a) {
     return unlocked(p_norm_q8, q, d, h.p, h.ld, x.p, x.ld, r.p, r.ld, w, n, k, real(a[5]), stream_of(a[0]));
 }
 
+// stream, dev, x, weight, residual (or None), eps, q, e, s, h (or None)
+int64_t add_rmsnorm_mxfp4(PyObject* const* a) {
+    const int64_t dev = integer(a[1]);
+    const auto [n, k] = extents(a[2], dev);
+    const Rows x = rows(a[2], "x", dev, n, k), r = rows_or_none(a[4], "residual", dev, n, k);
+    const Rows h = rows_or_none(a[9], "h", dev, n, k);
+    auto* q = (uint8_t*)packed(a[6], "q", at::kByte, dev, {n, k / 2});
+    auto* e = (uint8_t*)packed(a[7], "e", at::kByte, dev, {n, k / 32});
+    auto* s = (float*)packed(a[8], "s", at::kFloat, dev, {n});
+    const auto* w = (const float*)packed(a[3], "weight", at::kFloat, dev, {k});
+    return unlocked(p_norm_mx, q, e, s, h.p, h.ld, x.p, x.ld, r.p, r.ld, w, n, k, real(a[5]), stream_of(a[0]));
+}
+
+// Codes and scales of MXFP4 rows, any leading dimensions, contiguous.
+struct Mx {
+    uint8_t *q, *e;
+    int64_t rows, k;
+};
+Mx mx(PyObject* qo, const char* q_name, PyObject* eo, const char* e_name, int64_t dev) {
+    const at::Tensor &q = tensor(qo, q_name, at::kByte, dev), &e = tensor(eo, e_name, at::kByte, dev);
+    if (q.dim() < 1 || !q.is_contiguous()) misshapen(q, q_name, "contiguous [.., k/2]");
+    const int64_t last = q.size(-1);
+    if (e.dim() != q.dim() || !e.is_contiguous() || e.sizes().slice(0, e.dim() - 1) != q.sizes().slice(0, q.dim() - 1) ||
+        e.size(-1) * 16 != last)
+        misshapen(e, e_name, "contiguous [.., k/32] beside " + std::string(q_name) + " " + list_of(q.sizes()) + " of [.., k/2]");
+    int64_t n = 1;
+    for (int64_t i = 0; i + 1 < q.dim(); ++i) n *= q.size(i);
+    return Mx{(uint8_t*)q.data_ptr(), (uint8_t*)e.data_ptr(), n, 2 * last};
+}
+
+// stream, dev, x, q, e
+int64_t quantize_mxfp4(PyObject* const* a) {
+    const int64_t dev = integer(a[1]);
+    if (!THPVariable_Check(a[2])) refuse(PyExc_TypeError, "x must be a device (cuda/hip) tensor");
+    const at::ScalarType type = THPVariable_Unpack(a[2]).scalar_type();
+    if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16)
+        refuse(PyExc_TypeError, std::string("x must be float32, float16 or bfloat16, got ") + at::toString(type));
+    const at::Tensor& x = tensor(a[2], "x", type, dev);
+    if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1)) misshapen(x, "x", "[rows, k] with contiguous rows");
+    const int64_t n = x.size(0), k = x.size(1);
+    auto* q = (uint8_t*)packed(a[3], "q", at::kByte, dev, {n, k / 2});
+    auto* e = (uint8_t*)packed(a[4], "e", at::kByte, dev, {n, k / 32});
+    return unlocked(p_quantize_mx, q, e, (const void*)x.data_ptr(),
+                    (int)(type == at::kFloat ? QMM_MX_F32 : type == at::kHalf ? QMM_MX_F16 : QMM_MX_BF16),
+                    n > 1 ? x.stride(0) : k, n, k, stream_of(a[0]));
+}
+
+// stream, dev, q, e, out
+int64_t dequantize_mxfp4(PyObject* const* a) {
+    const int64_t dev = integer(a[1]);
+    const Mx m = mx(a[2], "q", a[3], "e", dev);
+    const at::Tensor& q = THPVariable_Unpack(a[2]);
+    std::vector<int64_t> shape(q.sizes().begin(), q.sizes().end());
+    shape.back() = m.k;
+    auto* out = (float*)packed(a[4], "out", at::kFloat, dev, shape);
+    return unlocked(p_dequantize_mx, out, (const uint8_t*)m.q, (const uint8_t*)m.e, m.rows, m.k, stream_of(a[0]));
+}
+
+// stream, dev, wq, we, xq, xe, x_scale (or None), out
+int64_t gemm_mxfp4(PyObject* const* a) {
+    const int64_t dev = integer(a[1]);
+    const Mx w = mx(a[2], "wq", a[3], "we", dev), x = mx(a[4], "xq", a[5], "xe", dev);
+    if (THPVariable_Unpack(a[2]).dim() != 2) misshapen(THPVariable_Unpack(a[2]), "wq", "[m, k/2]");
+    if (THPVariable_Unpack(a[4]).dim() != 2 || x.k != w.k)
+        misshapen(THPVariable_Unpack(a[4]), "xq", "[n, " + std::to_string(w.k / 2) + "]");
+    const auto* s = a[6] == Py_None ? nullptr : (const float*)packed(a[6], "x_scale", at::kFloat, dev, {x.rows});
+    const Rows out = rows(a[7], "out", dev, x.rows, w.rows);
+    return unlocked(p_gemm_mx, out.p, out.ld, (const uint8_t*)w.q, (const uint8_t*)w.e, (const uint8_t*)x.q,
+                    (const uint8_t*)x.e, s, w.rows, w.k, x.rows, stream_of(a[0]));
+}
+
 template <int64_t (*F)(PyObject* const*), Py_ssize_t N>
 PyMethodDef def(const char* name) {
     return PyMethodDef{name, (PyCFunction)(void (*)())method<F, N>, METH_FASTCALL, nullptr};
 }
-PyMethodDef g_methods[] = {def<bind, 6>("bind"),
+PyMethodDef g_methods[] = {def<bind, 10>("bind"),
                            def<device, 2>("device"),
                            def<paged_extend, 12>("paged_extend"),
                            def<kv_append, 6>("kv_append"),
                            def<paged_attention, 10>("paged_attention"),
                            def<add_rmsnorm, 8>("add_rmsnorm"),
                            def<add_rmsnorm_q8, 9>("add_rmsnorm_q8"),
+                           def<add_rmsnorm_mxfp4, 10>("add_rmsnorm_mxfp4"),
+                           def<quantize_mxfp4, 5>("quantize_mxfp4"),
+                           def<dequantize_mxfp4, 5>("dequantize_mxfp4"),
+                           def<gemm_mxfp4, 8>("gemm_mxfp4"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_step", "Decode step calls of libqmm", -1, g_methods};
 

@@ -444,8 +444,10 @@ int qmm_stream_loadonly(uint32_t* sink, const void* w, int64_t m, int64_t k,
  */
 
 /* Element kinds of a cache.  QMM_KV_Q8: int8 codes and one float scale per
- * (token, head): an element is scale * code, -127 <= code <= 127. */
-typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8 = 2 } qmm_kv_kind;
+ * (token, head): an element is scale * code, -127 <= code <= 127.
+ * QMM_KV_MXFP4: rows of head_dim MXFP4 values (qmm_quantize_mxfp4), head_dim/2
+ * bytes of codes and head_dim/32 scale bytes each. */
+typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8 = 2, QMM_KV_MXFP4 = 4 } qmm_kv_kind;
 
 /*
  * A paged key-value cache (a HOST struct; its pointers are DEVICE).  Element
@@ -453,13 +455,17 @@ typedef enum { QMM_KV_F16 = 0, QMM_KV_BF16 = 1, QMM_KV_Q8 = 2 } qmm_kv_kind;
  *     k[p*page_stride + h*head_stride + s*slot_stride + x]
  * and the same in v, so pages may hold heads outermost, tokens outermost, or
  * both caches in one tensor.  A token's slot number is p*page_size + s.
+ * (QMM_KV_MXFP4: two elements a byte, element x even in the low half; strides
+ * count elements there too.)
  *   k, v          16-byte aligned; strides in elements, each >= head_dim and a
  *                 multiple of 16 bytes, giving every row bytes of its own: a
  *                 row of k that meets one of v is QMM_ERR_ALIAS.
- *   k_scale, v_scale  QMM_KV_Q8 only (else ignored): float, strides in
- *                 elements, each >= 1, giving every scale a place of its own
- *                 (QMM_ERR_ALIAS where the two meet, or where either lies in
- *                 codes that leave no gaps).
+ *   k_scale, v_scale  QMM_KV_Q8 and QMM_KV_MXFP4 only (else ignored): float,
+ *                 strides in elements, each >= 1, giving every scale a place of
+ *                 its own (QMM_ERR_ALIAS where the two meet, or where either
+ *                 lies in codes that leave no gaps); QMM_KV_MXFP4: bytes, of
+ *                 any alignment, the head_dim/32 of a row side by side, strides
+ *                 in bytes, each >= head_dim/32.
  *   page_size     a power of two.  head_dim: a multiple of 32, at most 256
  *                 (QMM_ERR_K_ALIGN, QMM_ERR_RANGE).
  * Limits (QMM_ERR_RANGE): n_pages*page_size <= 2^30, n_kv <= 65535, 64 GiB
@@ -521,6 +527,7 @@ int qmm_paged_extend(int32_t* block_table, int64_t table_stride, int32_t* seq_le
  * qmm_quantize_q8_1 does per block.  A row with an infinity gets an infinite
  * scale, one with a NaN a NaN (its codes are 0): attention over it is then
  * non-finite in the heads that read it, as with the 16-bit kinds.
+ * QMM_KV_MXFP4: codes and scales as qmm_quantize_mxfp4 gives them.
  *   k, v    DEVICE float, n rows of n_kv*head_dim, ldk and ldv floats apart
  *           (multiples of 4; rows of a fused projection's output), 16-byte
  *           aligned.
@@ -547,8 +554,8 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * or value makes the outputs that it enters non-finite, except that a score
  * of -inf may count as a weight of zero; the same holds for scores beyond the
  * f32 range.
- * f32 arithmetic: f32 operands enter the matrix cores as two f16 (three
- * bf16) parts, products and sums are f32; the exponential and logarithm are
+ * f32 arithmetic: f32 operands enter the matrix cores as two f16 (a bf16 or
+ * MXFP4 cache: three bf16) parts, products and sums are f32; the exponential and logarithm are
  * the hardware's.  (f16 parts: an element of q is kept to 2^-38 of its head's
  * largest, a weight to 2^-39 of the largest.)  Finite elements and scores
  * give finite outputs.
@@ -609,6 +616,68 @@ int qmm_add_rmsnorm(float* y, int64_t ldy, float* h, int64_t ldh, const float* x
  */
 int qmm_add_rmsnorm_q8(int8_t* q, float* d, float* h, int64_t ldh, const float* x, int64_t ldx, const float* residual,
                        int64_t ldr, const float* weight, int64_t n, int64_t k, float eps, hipStream_t stream);
+
+/*
+ * Microscaled 4-bit floats (MXFP4, of the OCP Microscaling Formats
+ * specification).  A row of k values (k a multiple of 32) is k/2 bytes of E2M1
+ * codes (a sign bit over 0, 0.5, 1, 1.5, 2, 3, 4, 6), value 2j in the low half
+ * of byte j, and k/32 scale bytes, one per 32 consecutive values: a value is
+ * code * 2^(byte - 127), byte 255 is NaN.  Codes and scales are apart, rows of
+ * either without padding.
+ */
+
+/* Types of the values that qmm_quantize_mxfp4 takes. */
+typedef enum { QMM_MX_F32 = 0, QMM_MX_F16 = 1, QMM_MX_BF16 = 2 } qmm_mx_type;
+
+/*
+ * qmm_quantize_mxfp4: rows of values to MXFP4.  Per 32 values, exactly:
+ * e = floor(log2 max|x|) - 2, at least -127 (where all are 0 too), scale byte
+ * e + 127, codes x * 2^-e rounded to nearest, ties to the even code, to at most
+ * 6 in magnitude (a zero keeps its sign).  A block with an infinity or a NaN
+ * has scale byte 255 and codes 0.
+ *   q     DEVICE uint8[rows*k/2], 16-byte aligned.  e: DEVICE uint8[rows*k/32].
+ *   x     DEVICE values of the type, rows ldx >= k elements apart, 16-byte
+ *         aligned, ldx a multiple of 16 bytes.  Unknown type: QMM_ERR_QTYPE.
+ *   k     a multiple of 32 (QMM_ERR_K_ALIGN), below 2^31.
+ */
+int qmm_quantize_mxfp4(uint8_t* q, uint8_t* e, const void* x, int type, int64_t ldx, int64_t rows, int64_t k,
+                       hipStream_t stream);
+
+/*
+ * qmm_dequantize_mxfp4: the values that codes and scales stand for, as f32
+ * (exact; beyond f32 an infinity).
+ *   x     DEVICE float[rows*k], 16-byte aligned; q 16-byte aligned.
+ */
+int qmm_dequantize_mxfp4(float* x, const uint8_t* q, const uint8_t* e, int64_t rows, int64_t k, hipStream_t stream);
+
+/*
+ * qmm_gemm_mxfp4: the projection of MXFP4 activations by MXFP4 weights,
+ *     dst[j*ldd + i] = x_scale[j] * sum_c W[i][c] * X[j][c]    (x_scale NULL: 1)
+ * on the scaled 4-bit matrix instructions: exact products, f32 sums.  A NaN
+ * scale makes the outputs of its row NaN.
+ *   dst    DEVICE float, n rows ldd >= m apart, written; elements between m and
+ *          ldd are not.
+ *   wq, we DEVICE codes and scales of m rows of k; xq, xe those of n rows.  Codes
+ *          16-byte aligned, scales 4-byte.
+ *   x_scale  DEVICE float[n], or NULL: qmm_add_rmsnorm_mxfp4's factors.
+ *   k      a multiple of 32, at most 2^23; n at most 2^20 (QMM_ERR_RANGE).
+ * The sums' order depends on the sizes alone: identical calls are bit-identical.
+ */
+int qmm_gemm_mxfp4(float* dst, int64_t ldd, const uint8_t* wq, const uint8_t* we, const uint8_t* xq, const uint8_t* xe,
+                   const float* x_scale, int64_t m, int64_t k, int64_t n, hipStream_t stream);
+
+/*
+ * qmm_add_rmsnorm_mxfp4: qmm_add_rmsnorm with y in MXFP4.  1/rms is one factor
+ * of a whole row, so q and e are those of z = h * weight (each product rounded
+ * to f32), and s holds the rows' 1 / sqrt(mean h^2 + eps), for qmm_gemm_mxfp4's
+ * x_scale: y = s * z.
+ *   q     DEVICE uint8[n*k/2], 16-byte aligned.  e: DEVICE uint8[n*k/32].
+ *   s     DEVICE float[n].   k: a multiple of 32.
+ * Other arguments as qmm_add_rmsnorm.
+ */
+int qmm_add_rmsnorm_mxfp4(uint8_t* q, uint8_t* e, float* s, float* h, int64_t ldh, const float* x, int64_t ldx,
+                          const float* residual, int64_t ldr, const float* weight, int64_t n, int64_t k, float eps,
+                          hipStream_t stream);
 
 /* Packed bytes of one row of k weights; < 0 is -qmm_status on error.
  * (Sizes per the VARIANTS table of cera wgpu_gemm_bench.rs and memra
