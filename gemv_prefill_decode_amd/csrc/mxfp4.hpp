@@ -72,7 +72,9 @@ struct MxGemmArgs {
     int64_t ldd;
     int m, n, k;
 };
-void launch_gemm_mxfp4(const MxGemmArgs& a, int num_cu, hipStream_t st);
+// forced: the kernel to take where it can (tests and sweeps), or -1.
+void launch_gemm_mxfp4(const MxGemmArgs& a, int forced, int num_cu, hipStream_t st);
+int gemm_mxfp4_kernels();  // how many there are
 
 // The norm to MXFP4: codes of h * weight in q, their scales in e, 1/rms in d.
 struct NormMxArgs : NormArgs {

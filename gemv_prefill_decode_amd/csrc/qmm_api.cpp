@@ -1110,8 +1110,10 @@ int qmm_gemm_mxfp4(float* dst, int64_t ldd, const uint8_t* wq, const uint8_t* we
     if (!mul_ok(n, ldd, &span) || span > INT64_MAX / 4) return QMM_ERR_SHAPE;
     const Span ins[] = {{wq, m * k / 2}, {we, m * k / 32}, {xq, n * k / 2}, {xe, n * k / 32}, {x_scale, x_scale ? n * 4 : 0}};
     if (overlaps_any(dst, ((n - 1) * ldd + m) * 4, {ins[0], ins[1], ins[2], ins[3], ins[4]})) return QMM_ERR_ALIAS;
+    const int kernels = qmm::gemm_mxfp4_kernels(), forced = env_int("QMM_MX_KERNEL", kernels, 0, kernels - 1);
+    if (forced < 0) return QMM_ERR_RANGE;
     const qmm::MxGemmArgs a{dst, wq, we, xq, xe, x_scale, ldd, (int)m, (int)n, (int)k};
-    qmm::launch_gemm_mxfp4(a, dev_props().cu, stream);
+    qmm::launch_gemm_mxfp4(a, forced < kernels ? forced : -1, dev_props().cu, stream);
     return launch_status();
 }
 

@@ -661,7 +661,11 @@ int qmm_dequantize_mxfp4(float* x, const uint8_t* q, const uint8_t* e, int64_t r
  *          16-byte aligned, scales 4-byte.
  *   x_scale  DEVICE float[n], or NULL: qmm_add_rmsnorm_mxfp4's factors.
  *   k      a multiple of 32, at most 2^23; n at most 2^20 (QMM_ERR_RANGE).
+ * A cost model fitted to MI355X measurements picks one of 11 kernels (tiles
+ * from 16 x 16 to 256 x 256, with or without groups of waves that share a sum).
  * The sums' order depends on the sizes alone: identical calls are bit-identical.
+ * The environment variable QMM_MX_KERNEL=0..10 takes that one where it can run
+ * (tuning and tests only; malformed -> QMM_ERR_RANGE).
  */
 int qmm_gemm_mxfp4(float* dst, int64_t ldd, const uint8_t* wq, const uint8_t* we, const uint8_t* xq, const uint8_t* xe,
                    const float* x_scale, int64_t m, int64_t k, int64_t n, hipStream_t stream);

@@ -135,6 +135,38 @@ def test_gemm_is_exact_where_sums_are(m, k, n):
     assert np.array_equal(got, want * s[:, None])
 
 
+@pytest.mark.parametrize("kernel", range(11))
+def test_gemm_every_kernel(kernel, monkeypatch):
+    """Each kernel on the edges of every other's tiles: rows and tokens that end inside a tile, k that
+    ends inside a stage, a group of 512 and a wave's share."""
+    torch, qmm = _torch(), _qmm()
+    monkeypatch.setenv("QMM_MX_KERNEL", str(kernel))
+    for m, k, n in [(1, 32, 1), (17, 64, 3), (65, 480, 33), (130, 544, 257), (257, 1024, 129), (48, 1056, 64), (300, 2080, 20),
+                    (256, 1536, 512), (33, 5120, 5), (520, 288, 300)]:
+        gh.note(f"gemm_mxfp4 kernel {kernel} {m}x{k} n={n}")
+        rng = np.random.default_rng(m + k + n)
+        w, x = (rng.integers(0, 256, (r, k // 2), dtype=np.uint8) for r in (m, n))
+        we, xe = (rng.integers(127, 129, (r, k // 32), dtype=np.uint8) for r in (m, n))
+        out = torch.full((n + 1, m + 1), 7.0, device="cuda")
+        qmm.gemm_mxfp4(_dev(w), _dev(we), _dev(x), _dev(xe), out=out[:n, :m])
+        got = out.cpu().numpy()
+        assert np.array_equal(got[:n, :m], mxfp4.gemm(w, we, x, xe)[0]), (m, k, n)
+        assert (got[n] == 7).all() and (got[:, m] == 7).all()
+        if k > 1000:        # a NaN scale at the row's end stays in its row
+            we[m // 2, -1] = 255
+            got = qmm.gemm_mxfp4(_dev(w), _dev(we), _dev(x), _dev(xe)).cpu().numpy()
+            assert np.isnan(got[:, m // 2]).all() and np.isfinite(np.delete(got, m // 2, 1)).all()
+
+
+def test_gemm_malformed_kernel_choice(monkeypatch):
+    qmm = _qmm()
+    args = [_dev(np.zeros(s, np.uint8)) for s in ((2, 16), (2, 1), (3, 16), (3, 1))]
+    for bad in ("11", "-1", "x", "1 2"):
+        monkeypatch.setenv("QMM_MX_KERNEL", bad)
+        with pytest.raises(qmm.QmmError, match="8"):
+            qmm.gemm_mxfp4(*args)
+
+
 @pytest.mark.parametrize("m,k,n", [(40, 4608, 20), (300, 4096, 70), (130, 14336, 3), (300, 2080, 300), (16, 64, 16)])
 def test_gemm_is_within_its_bound(m, k, n):
     torch, qmm = _torch(), _qmm()
