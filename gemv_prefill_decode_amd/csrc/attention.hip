@@ -18,9 +18,7 @@
 // of two that cancel at the end; bf16 parts have f32's exponents and only stay
 // clear of its ends, keys and values reaching as far as f32's.  8-bit rows are
 // exact as f16 codes; a key's scale multiplies its score, a value's scale its
-// probability.  MXFP4 rows (mxfp4.hpp) become bf16 on their way into the matrix
-// cores, where a code times its block's power of two is exact, and are treated
-// as a bf16 cache from there on.
+// probability.
 //
 // Tiles.  A wave takes 32 tokens at a time: scores as K q^T (two 16-token
 // tiles: lane (c, i) = (lane / 16, lane % 16) gets head i's scores of tokens
@@ -145,8 +143,6 @@ __device__ __forceinline__ void ldg(uint32_t (&dst)[N], int at, const char* p, i
         dst[at] = v.x; dst[at + 1] = v.y;
     } else if (bytes == 4) {
         dst[at] = ldx<NT, uint32_t>(p);
-    } else if (bytes == 1) {
-        dst[at] = ldx<NT, uint8_t>(p);
     } else {
         dst[at] = ldx<NT, uint16_t>(p);
     }
@@ -154,18 +150,15 @@ __device__ __forceinline__ void ldg(uint32_t (&dst)[N], int at, const char* p, i
 
 // Eight f32 as f16 (bf16) parts: x = part 0 + part 1 (+ part 2) up to 2^-22
 // (2^-24) of |x|.
-// Kinds whose arithmetic is in bf16 parts.
-constexpr bool in_bf16(int kind) { return kind == KV_BF16 || kind == KV_MX4; }
-
 template <int KIND>
-__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&part)[in_bf16(KIND) ? 3 : 2]) {
-    constexpr int NS = in_bf16(KIND) ? 3 : 2;
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&part)[KIND == KV_BF16 ? 3 : 2]) {
+    constexpr int NS = KIND == KV_BF16 ? 3 : 2;
     float rest[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) rest[j] = x[j];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-        if constexpr (in_bf16(KIND)) {
+        if constexpr (KIND == KV_BF16) {
             bf16x8 v;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -187,7 +180,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&part)[in_bf1
 
 template <int KIND>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-    if constexpr (in_bf16(KIND))
+    if constexpr (KIND == KV_BF16)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -202,49 +195,20 @@ __device__ __forceinline__ uint32_t codes2(uint32_t bytes, bool high) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// The N scale bytes of an MXFP4 row, byte b in bits 8b of the pair.
-template <int N>
-__device__ __forceinline__ u32x2 scale_bytes(const uint8_t* p) {
-    uint32_t lo = 0, hi = 0;
-    if constexpr (N >= 4) __builtin_memcpy(&lo, p, 4);
-    if constexpr (N == 8) __builtin_memcpy(&hi, p + 4, 4);
-    constexpr int AT = N & 4, REST = N & 3;
-    uint32_t rest = 0;
-    if constexpr (REST >= 2) {
-        uint16_t h;
-        __builtin_memcpy(&h, p + AT, 2);
-        rest = h;
-    }
-    if constexpr (REST & 1) rest |= (uint32_t)p[AT + REST - 1] << (8 * (REST - 1));
-    if constexpr (REST > 0 && AT) hi = rest;
-    if constexpr (REST > 0 && !AT) lo = rest;
-    return u32x2{lo, hi};
-}
-// Scale of block b, 2^(byte - 127), as the scaled conversions take it.
-__device__ __forceinline__ float block_scale(u32x2 w, int b) {
-    return mx_scale(((b & 4 ? w.y : w.x) >> (8 * (b & 3))) & 255u);
-}
-// Codes 2 BYTE and 2 BYTE + 1 of a dword as bf16, exact.
-template <int BYTE>
-__device__ __forceinline__ uint32_t mx_bf16x2(uint32_t codes, float scale) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, BYTE));
-}
-
 // One wave's state over a segment (some tiles of one unit), head i = lane % 16:
 // acc[o][r] belongs to the value dimension of operand o that lane 4c + r loads.
 template <int KIND, int NB>
 struct Segment {
     static constexpr int D = 32 * NB;
-    static constexpr bool Q8 = KIND == KV_Q8, MX = KIND == KV_MX4;
-    static constexpr int NS = in_bf16(KIND) ? 3 : 2;
-    static constexpr int BITS = MX ? 4 : Q8 ? 8 : 16;  // of an element
-    static constexpr int ROW = D * BITS / 8;           // bytes of a row
-    static constexpr int KW = ROW / 16;                // dwords of a lane's share of a key tile row
+    static constexpr bool Q8 = KIND == KV_Q8;
+    static constexpr int NS = KIND == KV_BF16 ? 3 : 2;
+    static constexpr int ES = Q8 ? 1 : 2;          // bytes per element
+    static constexpr int KW = Q8 ? 2 * NB : 4 * NB;  // dwords of a lane's share of a key tile row
+    static constexpr int VW = Q8 ? (NB + 1) / 2 : NB;
     // A value row is read by 16 lanes in runs of 8 elements per lane (128
     // dimensions), then 4 (64) and 2 (32) as head_dim leaves them.
     static constexpr int N8 = NB / 4;
     static constexpr bool N4 = (NB & 2) != 0, N2 = (NB & 1) != 0;
-    static constexpr int VW = MX ? N8 + N4 + N2 : Q8 ? (NB + 1) / 2 : NB;
 
     f32x4 acc[2 * NB];
     float m, l;
@@ -257,12 +221,11 @@ struct Segment {
     // Rows of whole lines are read once and past the caches (non-temporal: 131071
     // tokens of f16 heads of 128 94.9 -> 91.1 us); rows that share lines are not
     // (2048 tokens x 64 of 8-bit heads of 96: 63 us, non-temporal 84).
-    static constexpr bool STREAM = ROW % 128 == 0;
+    static constexpr bool STREAM = D * ES % 128 == 0;
 
-    // A key row's 128-byte lines, then what is left: 64, 32 and 16 bytes.
-    static constexpr int LINES = ROW / 128;
-    static constexpr bool REST64 = (ROW & 64) != 0, REST32 = (ROW & 32) != 0, REST16 = (ROW & 16) != 0;
-    static constexpr int AT32 = 128 * LINES + 64 * REST64, AT16 = AT32 + 32 * REST32;  // where they begin
+    // A key row's 128-byte lines, then what is left: 64 and 32 bytes.
+    static constexpr int LINES = D * ES / 128;
+    static constexpr bool REST64 = (D * ES & 64) != 0, REST32 = (D * ES & 32) != 0;
 
     // The lane's share of 16 rows: row i (its operand row), which needs the
     // 16-byte chunks 2c and 2c + 1 of every line.  A load instruction takes
@@ -278,8 +241,7 @@ struct Segment {
             ldg<STREAM>(kr, 8 * n + 4, odd + at, 16);
         }
         if constexpr (REST64) ldg<STREAM>(kr, 8 * LINES, own + 128 * LINES + 16 * c, 16);
-        if constexpr (REST32) ldg<STREAM>(kr, AT32 / 16, own + AT32 + 8 * c, 8);
-        if constexpr (REST16) ldg<STREAM>(kr, AT16 / 16, own + AT16 + 4 * c, 4);
+        if constexpr (REST32) ldg<STREAM>(kr, 8 * LINES + (REST64 ? 4 : 0), own + D * ES - 32 + 8 * c, 8);
     }
     static __device__ __forceinline__ void settle(uint32_t (&kr)[KW], int i) {
         const bool odd = i & 1;
@@ -296,14 +258,6 @@ struct Segment {
             }
     }
     static __device__ __forceinline__ void load_v(uint32_t (&vr)[VW], const char* row, int i) {
-        if constexpr (MX) {
-#pragma unroll
-            for (int n = 0; n < N8; ++n) ldg<STREAM>(vr, n, row + 64 * n + 4 * i, 4);
-            if constexpr (N4) ldg<STREAM>(vr, N8, row + 64 * N8 + 2 * i, 2);
-            if constexpr (N2) ldg<STREAM>(vr, N8 + N4, row + 64 * N8 + 32 * N4 + i, 1);
-            return;
-        }
-        constexpr int ES = BITS / 8;
 #pragma unroll
         for (int n = 0; n < N8; ++n) ldg<STREAM>(vr, n * 2 * ES, row + ES * (128 * n + 8 * i), 8 * ES);
         if constexpr (N4) ldg<STREAM>(vr, N8 * 2 * ES, row + ES * (128 * N8 + 4 * i), 4 * ES);
@@ -311,21 +265,15 @@ struct Segment {
     }
     // first dimension of the eight that lane c's share of step s holds
     static __device__ __forceinline__ int kdim(int s, int c) {
-        constexpr int CH = 128 / BITS, PER = CH / 4;  // dimensions in a chunk; steps of a line
-        if (s < PER * LINES) return 8 * CH * (s / PER) + 2 * CH * c + 8 * (s % PER);
+        constexpr int CH = 16 / ES, PER = 32 / ES / 8;  // dimensions in a chunk; steps of a line
+        if (s < PER * LINES) return 128 / ES * (s / PER) + 2 * CH * c + 8 * (s % PER);
         s -= PER * LINES;
-        if (REST64 && s < PER / 2) return 8 * CH * LINES + CH * c + 8 * s;
-        if (REST64) s -= PER / 2;
-        // 32 bytes: 8-bit rows, MXFP4 rows (two steps); 16: MXFP4 rows
-        if (REST32 && s < PER / 4) return AT32 * 8 / BITS + CH / 2 * c + 8 * s;
-        return D - 32 + 8 * c;
+        if (REST64 && s < PER / 2) return 128 / ES * LINES + CH * c + 8 * s;
+        return D - 32 + 8 * c;  // 32 bytes: 8-bit rows
     }
-    // the key operand of step s; MXFP4: with the scale of its block
-    static __device__ __forceinline__ u32x4 key(const uint32_t (&kr)[KW], int s, float scale = 1.0f) {
-        if constexpr (MX) {
-            return u32x4{mx_bf16x2<0>(kr[s], scale), mx_bf16x2<1>(kr[s], scale), mx_bf16x2<2>(kr[s], scale),
-                         mx_bf16x2<3>(kr[s], scale)};
-        } else if constexpr (Q8) {
+    // the key operand of step s
+    static __device__ __forceinline__ u32x4 key(const uint32_t (&kr)[KW], int s) {
+        if constexpr (Q8) {
             const uint32_t x = kr[2 * s] ^ SIGNS, y = kr[2 * s + 1] ^ SIGNS;
             return u32x4{codes2(x, false), codes2(x, true), codes2(y, false), codes2(y, true)};
         } else {
@@ -352,18 +300,6 @@ struct Segment {
         return u32x4{out[0], out[1], out[2], out[3]};
     }
 
-    // MXFP4: the value operands o and o + 1 (o even), from dword w of the rows, its byte BYTE
-    template <int BYTE>
-    static __device__ __forceinline__ void value2(const uint32_t (&vr)[8][VW], int w, const float (&scale)[8], u32x4* lo,
-                                                  u32x4* hi) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t a = mx_bf16x2<BYTE>(vr[2 * j][w], scale[2 * j]), b = mx_bf16x2<BYTE>(vr[2 * j + 1][w], scale[2 * j + 1]);
-            (*lo)[j] = __builtin_amdgcn_perm(b, a, 0x05040100u);
-            (*hi)[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-        }
-    }
-
     // Tiles [t, t + n) of sequence b (len tokens) for `rows` heads from query head head0.
     __device__ __forceinline__ void run(const AttnArgs& a, int b, int len, int kvh, int head0, int rows, int t, int n) {
         const int lane = threadIdx.x & 63, c = lane >> 4, i = lane & 15;
@@ -380,10 +316,9 @@ struct Segment {
         const char* kb = (const char*)a.k + (int64_t)kvh * a.head_bytes;
         const char* vb = (const char*)a.v + (int64_t)kvh * a.head_bytes;
         const float* sb = Q8 ? ((lane & 32) ? a.v_scale : a.k_scale) + (int64_t)kvh * a.scale_head : nullptr;
-        const uint8_t* mb = MX ? (const uint8_t*)((lane & 32) ? a.v_scale : a.k_scale) + (int64_t)kvh * a.scale_head : nullptr;
         const int* table = a.table + (int64_t)b * a.table_stride;
         bool bad = false;
-        const float pbits = in_bf16(KIND) ? (float)-log2_up(len) : Q8 ? 0.0f : PBITS;
+        const float pbits = KIND == KV_BF16 ? (float)-log2_up(len) : Q8 ? 0.0f : PBITS;
 
         // page id of the lane's token (lane % 32) of tile tt; tokens behind the last read as the last
         auto token = [&](int tt) {
@@ -393,14 +328,12 @@ struct Segment {
         auto page_id = [&](int tt) { return table[token(tt) >> a.page_log2]; };
         uint32_t off;        // the row of the lane's token, in 16-byte units from the head's first
         float sc = 0.0f;     // its key (lanes 0..31) or value scale
-        u32x2 mx = {0, 0};   // MXFP4: its blocks' scales
         auto locate = [&](int id, int tt) {
             const bool out = (uint32_t)id >= (uint32_t)a.n_pages;
             bad |= out;
             const uint32_t pg = out ? 0u : (uint32_t)id, slot = (uint32_t)token(tt) & (uint32_t)(a.page_size - 1);
             off = pg * a.page_units + slot * a.slot_units;
             if constexpr (Q8) sc = sb[(int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot];
-            if constexpr (MX) mx = scale_bytes<NB>(mb + (int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot);
         };
         auto row_of = [&](const char* base, int src) {
             return base + ((uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(4 * src, (int)off) << 4);
@@ -410,13 +343,7 @@ struct Segment {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 load_k(kr[h], row_of(kb, 16 * h + (i & ~1)), row_of(kb, 16 * h + (i | 1)),
-                       REST64 || REST32 || REST16 ? row_of(kb, 16 * h + i) : kb, c, i);
-        };
-        // the scales of the token that lane src located
-        auto scales_of = [&](int src) {
-            u32x2 w = {(uint32_t)__builtin_amdgcn_ds_bpermute(4 * src, (int)mx.x), 0};
-            if constexpr (NB > 4) w.y = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * src, (int)mx.y);
-            return w;
+                       REST64 || REST32 ? row_of(kb, 16 * h + i) : kb, c, i);
         };
         auto tok_of = [&](int j) { return (j < 4 ? 0 : 12) + 4 * c + j; };  // token of the lane's k index j
         auto load_values = [&]() {
@@ -449,7 +376,7 @@ struct Segment {
             top = max_c(top);
             // q's factor, a power of two: its exponent field
             int e;
-            if constexpr (in_bf16(KIND)) {
+            if constexpr (KIND == KV_BF16) {
                 // 2^-12, so that the sum of products passes f32 no sooner than the score, but at
                 // least what takes the largest to 2^-60: its parts are normal numbers
                 e = 194 - (int)(ubits(top) >> 23);
@@ -475,30 +402,12 @@ struct Segment {
             f32x4 s4[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
             settle(kr[0], i);
             settle(kr[1], i);
-            if constexpr (MX) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const u32x2 w = scales_of(16 * h + i);
+            for (int s = 0; s < NB; ++s)
 #pragma unroll
-                    for (int s = 0; s < NB; ++s) {
-                        const u32x4 k = key(kr[h], s, block_scale(w, kdim(s, c) / 32));
+                for (int p = 0; p < NS; ++p)
 #pragma unroll
-                        for (int p = 0; p < NS; ++p) s4[h] = mfma<KIND>(k, qp[s][p], s4[h]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < NB; ++s)
-#pragma unroll
-                    for (int p = 0; p < NS; ++p)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) s4[h] = mfma<KIND>(key(kr[h], s), qp[s][p], s4[h]);
-            }
-            u32x2 vmx[8];  // MXFP4: the scales of the lane's eight value rows
-            if constexpr (MX) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) vmx[j] = scales_of(32 + tok_of(j));
-            }
+                    for (int h = 0; h < 2; ++h) s4[h] = mfma<KIND>(key(kr[h], s), qp[s][p], s4[h]);
             float s[8], vs[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -565,39 +474,11 @@ struct Segment {
             }
             u32x4 pp[NS];
             split8<KIND>(p, pp);
-            if constexpr (MX) {
-                // dword w of the value rows: N of its bytes, two operands each, from operand o on, of block b
-                auto dword = [&](auto n, int w, int o, int b) {
-                    float scale[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) scale[j] = block_scale(vmx[j], b);
-                    auto byte = [&](auto at) {
-                        u32x4 lo, hi;
-                        value2<at>(vr, w, scale, &lo, &hi);
+            for (int o = 0; o < 2 * NB; ++o) {
+                const u32x4 v = value(vr, o);
 #pragma unroll
-                        for (int q = 0; q < NS; ++q) {
-                            acc[o + 2 * at] = mfma<KIND>(lo, pp[q], acc[o + 2 * at]);
-                            acc[o + 2 * at + 1] = mfma<KIND>(hi, pp[q], acc[o + 2 * at + 1]);
-                        }
-                    };
-                    byte(std::integral_constant<int, 0>{});
-                    if constexpr (n > 1) byte(std::integral_constant<int, 1>{});
-                    if constexpr (n > 2) {
-                        byte(std::integral_constant<int, 2>{});
-                        byte(std::integral_constant<int, 3>{});
-                    }
-                };
-#pragma unroll
-                for (int n = 0; n < N8; ++n) dword(std::integral_constant<int, 4>{}, n, 8 * n, 4 * n + i / 4);
-                if constexpr (N4) dword(std::integral_constant<int, 2>{}, N8, 8 * N8, 4 * N8 + i / 8);
-                if constexpr (N2) dword(std::integral_constant<int, 1>{}, N8 + N4, 2 * NB - 2, NB - 1);
-            } else {
-#pragma unroll
-                for (int o = 0; o < 2 * NB; ++o) {
-                    const u32x4 v = value(vr, o);
-#pragma unroll
-                    for (int q = 0; q < NS; ++q) acc[o] = mfma<KIND>(v, pp[q], acc[o]);
-                }
+                for (int q = 0; q < NS; ++q) acc[o] = mfma<KIND>(v, pp[q], acc[o]);
             }
             if (more) load_values();
         }
@@ -614,6 +495,453 @@ struct Segment {
     }
 
     // f(dimension, the sums of it and the next one or three, times w) over the lane's sums
+    template <typename F>
+    __device__ __forceinline__ void each(float w, F f) const {
+        const int rho = 4 * ((threadIdx.x >> 4) & 3);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+#pragma unroll
+            for (int o = 0; o < 8 * N8; o += 4)
+                f(128 * (o / 8) + 8 * (rho + r) + o % 8,
+                  f32x4{acc[o][r] * w, acc[o + 1][r] * w, acc[o + 2][r] * w, acc[o + 3][r] * w});
+            if constexpr (N4) {
+                constexpr int o = 8 * N8;
+                f(128 * N8 + 4 * (rho + r), f32x4{acc[o][r] * w, acc[o + 1][r] * w, acc[o + 2][r] * w, acc[o + 3][r] * w});
+            }
+            if constexpr (N2) {
+                constexpr int o = 2 * NB - 2;
+                f(D - 32 + 2 * (rho + r), f32x2{acc[o][r] * w, acc[o + 1][r] * w});
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------ MXFP4 rows
+// The N scale bytes of an MXFP4 row, byte b in bits 8b of the pair.
+template <int N>
+__device__ __forceinline__ u32x2 scale_bytes(const uint8_t* p) {
+    uint32_t lo = 0, hi = 0;
+    if constexpr (N >= 4) __builtin_memcpy(&lo, p, 4);
+    if constexpr (N == 8) __builtin_memcpy(&hi, p + 4, 4);
+    constexpr int AT = N & 4, REST = N & 3;
+    uint32_t rest = 0;
+    if constexpr (REST >= 2) {
+        uint16_t h;
+        __builtin_memcpy(&h, p + AT, 2);
+        rest = h;
+    }
+    if constexpr (REST & 1) rest |= (uint32_t)p[AT + REST - 1] << (8 * (REST - 1));
+    if constexpr (REST > 0 && AT) hi = rest;
+    if constexpr (REST > 0 && !AT) lo = rest;
+    return u32x2{lo, hi};
+}
+// Scale of block b as the scaled conversions take it: byte b in the exponent's
+// place, the rest does not matter (mxfp4.hpp).
+__device__ __forceinline__ float block_scale(u32x2 w, int b) {
+    const uint32_t v = b & 4 ? w.y : w.x;
+    return fbits(__builtin_amdgcn_alignbit(v, v, (uint32_t)(8 * (b & 3) + 9) & 31u));
+}
+// Codes 2 BYTE and 2 BYTE + 1 of a dword as bf16, exact.
+template <int BYTE>
+__device__ __forceinline__ uint32_t mx_bf16x2(uint32_t codes, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, BYTE));
+}
+// Eight f32 as three bf16 parts, truncated: upper halves are put together two
+// at a time, and three of 8 bits each are all of x.
+__device__ __forceinline__ void cut8(const float (&x)[8], u32x4 (&part)[3]) {
+    float rest[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rest[j] = x[j];
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            part[s][j] = __builtin_amdgcn_perm(ubits(rest[2 * j + 1]), ubits(rest[2 * j]), 0x07060302u);
+            rest[2 * j] -= fbits(ubits(rest[2 * j]) & 0xffff0000u);
+            rest[2 * j + 1] -= fbits(ubits(rest[2 * j + 1]) & 0xffff0000u);
+        }
+}
+// v of lane J of each 16 lanes, in all of them
+template <int J>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + J, 0xf, 0xf, true);  // row_newbcast:J
+}
+
+template <typename F>
+__device__ __forceinline__ void for_eight(F f) {
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
+    f(std::integral_constant<int, 4>{});
+    f(std::integral_constant<int, 5>{});
+    f(std::integral_constant<int, 6>{});
+    f(std::integral_constant<int, 7>{});
+}
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
+
+// The E2M3 part of 32 values over a scale (value 2 z from even[z], 2 z + 1 from
+// odd[z]), rounded to nearest; they keep what is left.  The conversions write
+// their first results before they have read their last operands, which their
+// builtins do not tell the register allocation: the output has to be marked so.
+// (The wait is for the matrix core that may read the codes next.)
+__device__ __forceinline__ u32x6 e2m3_part(f32x16& even, f32x16& odd, float scale, bool more) {
+    u32x6 code;
+    asm("v_cvt_scalef32_2xpk16_fp6_f32 %0, %1, %2, %3\n\ts_nop 7" : "=&v"(code) : "v"(even), "v"(odd), "v"(scale));
+    if (more) {
+        f32x32 value;
+        asm("v_cvt_scalef32_pk32_f32_fp6 %0, %1, %2" : "=&v"(value) : "v"(code), "v"(scale));
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+            even[z] -= value[2 * z];
+            odd[z] -= value[2 * z + 1];
+        }
+    }
+    return code;
+}
+// sum += 16 key rows (E2M1 and a scale byte per lane) x 16 heads (an E2M3 part, byte S of its scales), 128 deep
+template <int S>
+__device__ __forceinline__ f32x4 mfma_parts(u32x4 k, uint32_t ks, u32x6 q, uint32_t qe, f32x4 sum) {
+    const i32x8 x = {(int)k.x, (int)k.y, (int)k.z, (int)k.w, 0, 0, 0, 0};
+    const i32x8 y = {(int)q[0], (int)q[1], (int)q[2], (int)q[3], (int)q[4], (int)q[5], 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, sum, 4, 2, 0, (int)ks, S, (int)qe);
+}
+
+// Segment for MXFP4 rows.  The tile, its lanes and acc are Segment's.
+//
+// Scores: v_mfma_scale_f32_16x16x128_f8f6f4 takes the key rows' codes and scales
+// as they are, lane (c, i) block 4 g + c of row i, against q in six E2M3 parts, each
+// with a scale per block: their sum is x up to 2^-30 of its block's largest.  (Key
+// codes made bf16 against q in three bf16 parts: 24 matrix instructions for 12 at a
+// head of 128 and 34 more of the vector ALUs, which are the busier.  131071 tokens of
+// 8 heads of 128 took 51.0 us that way, 48.2 this; 61 ragged sequences of up to 16384
+// 118.6 and 111.7.)
+//
+// Values become bf16 on their way into the matrix cores, where a code times its
+// block's power of two is exact, and p has three bf16 parts, as for a bf16 cache:
+// a scale per token and block lies along the sum, where the matrix cores take none.
+//
+// Bounds: at d 128 about 60 of 100 cycles of the vector ALUs and 30 of the matrix
+// cores with two waves a SIMD; the rows alone take 83% of the time.  More tiles in
+// flight or a third work group a CU gave nothing.
+//
+// WHOLE: pages of 16 tokens or more, so that a half tile's rows lie in one page, and
+// an address is a scalar base and a lane's constant; else each row is found by itself.
+template <int NB, bool WHOLE>
+struct SegmentMx {
+    static constexpr int D = 32 * NB;
+    static constexpr int N8 = NB / 4;
+    static constexpr bool N4 = (NB & 2) != 0, N2 = (NB & 1) != 0;
+    static constexpr int VW = N8 + N4 + N2;
+    static constexpr int TILES = NB <= 4 ? 2 : 1;  // tiles in registers
+    static constexpr int NG = (NB + 3) / 4;        // scaled instructions for a part of a score
+    static constexpr int NP = 6;                   // parts of q
+
+    f32x4 acc[2 * NB];
+    float m, l;
+
+    // Rows of one tile: the lane's share.
+    struct Tile {
+        u32x4 k[2][NG];      // of row i of each half, block 4 g + c
+        uint32_t ks[2][NG];  // and its scale byte
+        uint32_t v[8][VW];   // rows tok_of(j)
+        u32x2 vs;            // scales of row tok_of(i % 8)
+    };
+    // block of group g in lane c; those past the last are read as the last, and q's are zero
+    static __device__ __forceinline__ int block(int g, int c) { return 4 * g + c < NB ? 4 * g + c : NB - 1; }
+    static __device__ __forceinline__ void load_k_row(u32x4 (&k)[NG], uint32_t (&ks)[NG], const char* row, const uint8_t* scales, int c) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            k[g] = *(const u32x4*)(row + 16 * block(g, c));
+            ks[g] = scales[block(g, c)];
+        }
+    }
+
+    __device__ __forceinline__ void run(const AttnArgs& a, int b, int len, int kvh, int head0, int rows, int t, int n) {
+        const int lane = threadIdx.x & 63, c = lane >> 4, i = lane & 15;
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int o = 0; o < 2 * NB; ++o) acc[o] = f32x4{0, 0, 0, 0};
+        if (len <= 0) {
+            l = len < 0 ? NAN : 0.0f;
+            return;
+        }
+        const char* kb = (const char*)a.k + (int64_t)kvh * a.head_bytes;
+        const char* vb = (const char*)a.v + (int64_t)kvh * a.head_bytes;
+        const uint8_t* ksb = (const uint8_t*)a.k_scale + (int64_t)kvh * a.scale_head;
+        const uint8_t* vsb = (const uint8_t*)a.v_scale + (int64_t)kvh * a.scale_head;
+        const int* table = a.table + (int64_t)b * a.table_stride;
+        bool bad = false;
+        const float pbits = (float)-log2_up(len);
+        const int mask = a.page_size - 1;
+
+        auto tok_of = [&](int j) { return (j < 4 ? 0 : 12) + 4 * c + j; };  // token of the lane's k index j
+        auto load_v_row = [&](uint32_t (&v)[VW], const char* row) {
+#pragma unroll
+            for (int g = 0; g < N8; ++g) v[g] = *(const uint32_t*)(row + 64 * g + 4 * i);
+            if constexpr (N4) v[N8] = *(const uint16_t*)(row + 64 * N8 + 2 * i);
+            if constexpr (N2) v[N8 + N4] = *(const uint8_t*)(row + 64 * N8 + 32 * N4 + i);
+        };
+        // page ids of a tile: of its halves' first tokens (even and odd lanes), or of the lane's rows
+        struct Ids {
+            int id[3];
+        };
+        auto clamp_tok = [&](int tok) { return tok < len ? tok : len - 1; };
+        auto page_ids = [&](int tt) {
+            Ids p;
+            if constexpr (WHOLE) {
+                p.id[0] = table[clamp_tok(TILE * tt + 16 * (lane & 1)) >> a.page_log2];
+            } else {
+                p.id[0] = table[clamp_tok(TILE * tt + i) >> a.page_log2];
+                p.id[1] = table[clamp_tok(TILE * tt + 16 + i) >> a.page_log2];
+                p.id[2] = table[clamp_tok(TILE * tt + tok_of(i & 7)) >> a.page_log2];
+            }
+            return p;
+        };
+        auto checked = [&](int id) {
+            const bool out = (uint32_t)id >= (uint32_t)a.n_pages;
+            bad |= out;
+            return out ? 0u : (uint32_t)id;
+        };
+        const uint32_t sb = a.slot_units << 4, ss = (uint32_t)a.scale_slot;
+        // WHOLE: the first row of half h's 16 (the clamped token's), and its scales
+        auto half_rows = [&](const Ids& p, int tt, int h, int64_t* off, int64_t* soff) {
+            const uint32_t pg = checked(__builtin_amdgcn_readlane(p.id[0], h));
+            const uint32_t slot = (uint32_t)(clamp_tok(TILE * tt + 16 * h) & mask & ~15);
+            *off = (int64_t)((uint64_t)(pg * a.page_units + slot * a.slot_units) << 4);
+            *soff = (int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot;
+        };
+        // each row by itself
+        auto one_row = [&](int id, int tok, uint32_t* off, int64_t* soff) {
+            const uint32_t pg = checked(id), slot = (uint32_t)(tok & mask);
+            *off = pg * a.page_units + slot * a.slot_units;
+            *soff = (int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot;
+        };
+        auto load_keys = [&](Tile& x, const Ids& p, int tt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                int64_t soff;
+                if constexpr (WHOLE) {  // rows behind the last token are masked by their scores
+                    int64_t off;
+                    half_rows(p, tt, h, &off, &soff);
+                    load_k_row(x.k[h], x.ks[h], kb + off + (uint32_t)i * sb, ksb + soff + (uint32_t)i * ss, c);
+                } else {
+                    uint32_t off;
+                    one_row(p.id[h], clamp_tok(TILE * tt + 16 * h + i), &off, &soff);
+                    load_k_row(x.k[h], x.ks[h], kb + ((uint64_t)off << 4), ksb + soff, c);
+                }
+            }
+        };
+        auto load_values = [&](Tile& x, const Ids& p, int tt) {
+            if constexpr (WHOLE) {
+                int64_t off[2], soff[2];
+                half_rows(p, tt, 0, &off[0], &soff[0]);
+                half_rows(p, tt, 1, &off[1], &soff[1]);
+                const int mine = (i >> 2) & 1, left = len - TILE * tt - 1;
+                if (left >= TILE - 1) {
+                    x.vs = scale_bytes<NB>(vsb + (mine ? soff[1] : soff[0]) + (uint32_t)(4 * c + (i & 3)) * ss);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) load_v_row(x.v[j], vb + off[j >> 2] + (uint32_t)(j & 3) * sb + (uint32_t)(4 * c) * sb);
+                } else {
+                    // row r of half h; rows behind the last are read as the last (in half 1's place, where
+                    // it has none, lie the last token's 16)
+                    auto row = [&](int r, int h) {
+                        const int most = left - 16 * h;
+                        return (uint32_t)(most < 0 ? left & 15 : r < most ? r : most);
+                    };
+                    x.vs = scale_bytes<NB>(vsb + (mine ? soff[1] : soff[0]) + row(4 * c + (i & 3), mine) * ss);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) load_v_row(x.v[j], vb + off[j >> 2] + row(4 * c + (j & 3), j >> 2) * sb);
+                }
+            } else {
+                uint32_t off;
+                int64_t soff;
+                one_row(p.id[2], clamp_tok(TILE * tt + tok_of(i & 7)), &off, &soff);
+                x.vs = scale_bytes<NB>(vsb + soff);
+                auto each_row = [&](auto j) { load_v_row(x.v[j], vb + ((uint64_t)row_lane<j>(off) << 4)); };
+                for_eight(each_row);
+            }
+        };
+
+        Tile tile[TILES];
+        Ids ids = page_ids(t);
+        // tile `it`, if there is one, and the page ids of the one after
+        auto fetch = [&](Tile& x, int it) {
+            if (it < n) {
+                load_keys(x, ids, t + it);
+                load_values(x, ids, t + it);
+                if (it + 1 < n) ids = page_ids(t + it + 1);
+            }
+        };
+#pragma unroll
+        for (int z = 0; z < (TILES > 1 ? TILES - 1 : 1); ++z) fetch(tile[z], z);
+        // the query heads, split; lanes past the last head, and blocks past the last, hold zeros
+        u32x6 qp[NG][NP];
+        uint32_t qe[NG][2];  // the parts' scale bytes
+        float qs;
+        {
+            const float* qrow = a.q + (int64_t)b * a.q_stride + (int64_t)(head0 + (i < rows ? i : 0)) * D;
+            f32x16 even[NG], odd[NG];
+            float top = 0.0f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const bool in = i < rows && 4 * g + c < NB;
+                const f32x4* p = (const f32x4*)(qrow + 32 * block(g, c));
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    const f32x4 v = in ? p[z] : f32x4{0, 0, 0, 0};
+                    even[g][2 * z] = v.x;
+                    odd[g][2 * z] = v.y;
+                    even[g][2 * z + 1] = v.z;
+                    odd[g][2 * z + 1] = v.w;
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+                }
+            }
+            top = max_c(top);
+            // q's factor: 2^-12, so that the sum of products passes f32 no sooner than the score, but at
+            // least what takes the largest to 2^-60, far from the smallest scale; the scale's sign goes along
+            int e = 194 - (int)(ubits(top) >> 23);
+            e = e < 115 ? 115 : e;
+            const float f = fbits((uint32_t)e << 23 | (a.scale < 0.0f ? 0x80000000u : 0u));
+            qs = fbits((uint32_t)(254 - e) << 23) * fabsf(a.scale) * LOG2E;  // scale * log2(e) may pass f32
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t bits = 0;
+#pragma unroll
+                for (int z = 0; z < 16; ++z) {
+                    even[g][z] *= f;
+                    odd[g][z] *= f;
+                    bits = mx_larger(bits, mx_larger(mx_magnitude(even[g][z]), mx_magnitude(odd[g][z])));
+                }
+                // the first part's scale takes the block's largest below 4, the next are 2^-5 of the one before
+                const uint32_t top_e = bits >> 23, e0 = top_e > 26 ? top_e - 1 : 25;
+                qe[g][0] = top_e == 255 ? 0xffffffffu : e0 * 0x01010101u - 0x0f0a0500u;
+                qe[g][1] = top_e == 255 ? 0xffffffffu : (e0 - 20) | (e0 - 25) << 8;
+#pragma unroll
+                for (int p = 0; p < NP; ++p) qp[g][p] = e2m3_part(even[g], odd[g], fbits((e0 - 5 * p) << 23), p + 1 < NP);
+            }
+        }
+
+        auto work = [&](const Tile& x, int tt, auto prefetch) {
+            f32x4 raw[2] = {};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                auto part = [&](auto p) {
+                    raw[0] = mfma_parts<p & 3>(x.k[0][g], x.ks[0][g], qp[g][p], qe[g][p / 4], raw[0]);
+                    raw[1] = mfma_parts<p & 3>(x.k[1][g], x.ks[1][g], qp[g][p], qe[g][p / 4], raw[1]);
+                };
+                part(std::integral_constant<int, 0>{});
+                part(std::integral_constant<int, 1>{});
+                part(std::integral_constant<int, 2>{});
+                part(std::integral_constant<int, 3>{});
+                part(std::integral_constant<int, 4>{});
+                part(std::integral_constant<int, 5>{});
+            }
+            prefetch();
+            float s[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = raw[j / 4][j % 4];
+            const int left = len - TILE * tt;
+            if (left < TILE) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (tok_of(j) >= left) s[j] = -INFINITY;
+            }
+            float top = s[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = fmaxf(top, s[j]);
+            top = fmaxf(m, max_c(top) * qs);  // qs is not negative
+            const float base = top == -INFINITY ? 0.0f : top, shift = pbits - base;
+            const float alpha = __builtin_amdgcn_exp2f(m - base);
+            m = top;
+            float p[8], sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], qs, shift));
+            if (left < TILE) {  // (a scale of 0 makes NaN of -inf)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    asm volatile("" : "+v"(p[j]));  // stays a branch
+                    if (tok_of(j) >= left) p[j] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += p[j];
+            l = l * alpha + sum;
+            if (__any(alpha != 1.0f)) {
+#pragma unroll
+                for (int o = 0; o < 2 * NB; ++o) acc[o] *= alpha;
+            }
+            u32x4 pp[3];
+            cut8(p, pp);
+            // the scales of the lane's eight value rows
+            u32x2 vs[8];
+            auto spread = [&](auto j) {
+                vs[j].x = row_lane<j>(x.vs.x);
+                vs[j].y = NB > 4 ? row_lane<j>(x.vs.y) : 0u;
+            };
+            for_eight(spread);
+            // dword w of the value rows: N of its bytes, two operands each, from operand o on, of block blk
+            auto dword = [&](auto n, int w, int o, int blk) {
+                float scale[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) scale[j] = block_scale(vs[j], blk);
+                auto byte = [&](auto at) {
+                    u32x4 lo, hi;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t y = mx_bf16x2<at>(x.v[2 * j][w], scale[2 * j]), z = mx_bf16x2<at>(x.v[2 * j + 1][w], scale[2 * j + 1]);
+                        lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
+                        hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        acc[o + 2 * at] = mfma<KV_BF16>(lo, pp[q], acc[o + 2 * at]);
+                        acc[o + 2 * at + 1] = mfma<KV_BF16>(hi, pp[q], acc[o + 2 * at + 1]);
+                    }
+                };
+                byte(std::integral_constant<int, 0>{});
+                if constexpr (n > 1) byte(std::integral_constant<int, 1>{});
+                if constexpr (n > 2) {
+                    byte(std::integral_constant<int, 2>{});
+                    byte(std::integral_constant<int, 3>{});
+                }
+            };
+#pragma unroll
+            for (int g = 0; g < N8; ++g) dword(std::integral_constant<int, 4>{}, g, 8 * g, 4 * g + i / 4);
+            if constexpr (N4) dword(std::integral_constant<int, 2>{}, N8, 8 * N8, 4 * N8 + i / 8);
+            if constexpr (N2) dword(std::integral_constant<int, 1>{}, N8 + N4, 2 * NB - 2, NB - 1);
+        };
+        // The rows of TILES - 1 tiles are on their way behind the arithmetic of one; where there is room
+        // for one tile, its registers take the next one's as soon as they are read.
+        if constexpr (TILES > 1) {
+            for (int it = 0; it < n; it += TILES)
+#pragma unroll
+                for (int z = 0; z < TILES; ++z)
+                    if (it + z < n) {
+                        fetch(tile[(z + TILES - 1) % TILES], it + z + TILES - 1);
+                        work(tile[z], t + it + z, [] {});
+                    }
+        } else {
+            for (int it = 0; it < n; ++it) {
+                const Ids mine = ids;
+                work(tile[0], t + it, [&] {
+                    if (it + 1 < n) {
+                        load_keys(tile[0], mine, t + it + 1);
+                        if (it + 2 < n) ids = page_ids(t + it + 2);
+                    }
+                });
+                if (it + 1 < n) load_values(tile[0], mine, t + it + 1);
+            }
+        }
+        if (__any(bad)) l = NAN;
+        l = sum_c(l);
+    }
+
     template <typename F>
     __device__ __forceinline__ void each(float w, F f) const {
         const int rho = 4 * ((threadIdx.x >> 4) & 3);
@@ -718,7 +1046,8 @@ __device__ __forceinline__ int cut(const AttnArgs& a, int j, int w, Run* run) {
     return chunk;
 }
 
-template <int KIND, int NB>
+// WHOLE: MXFP4 rows on pages of 16 tokens or more.
+template <int KIND, int NB, bool WHOLE = false>
 __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(const AttnArgs a) {
     constexpr int D = 32 * NB;
     extern __shared__ __attribute__((aligned(16))) float parts[];  // [wave][2] parts
@@ -754,7 +1083,7 @@ __global__ __launch_bounds__(256, occupancy(KIND, NB)) void paged_attn_kernel(co
         const int n = (left < nt ? left : nt) - t;
         if (n <= 0) break;  // the run ends in the unit's first places: the next one starts it
         const Unit u = unit_of(a, hs, b);
-        Segment<KIND, NB> seg;
+        std::conditional_t<KIND == KV_MX4, SegmentMx<NB, WHOLE>, Segment<KIND == KV_MX4 ? (int)KV_BF16 : KIND, NB>> seg;
         seg.run(a, b, len, u.kvh, u.head0, u.rows, t, n);
         const int i = lane & 15;
         if (n == nt) {  // the whole unit: its outputs
@@ -955,13 +1284,13 @@ __global__ __launch_bounds__(256) void paged_attn_join_kernel(const AttnArgs a) 
     }
 }
 
-template <int KIND, int NB>
+template <int KIND, int NB, bool WHOLE = false>
 void launch(const AttnArgs& a, hipStream_t st) {
     const size_t lds = (size_t)8 * part_floats(a.heads_per_block, 32 * NB) * sizeof(float);
     if (lds > 64 * 1024)
-        (void)hipFuncSetAttribute((const void*)paged_attn_kernel<KIND, NB>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        (void)hipFuncSetAttribute((const void*)paged_attn_kernel<KIND, NB, WHOLE>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     const dim3 grid = a.per_unit ? dim3((unsigned)a.batch, (unsigned)a.head_spaces) : dim3((unsigned)a.groups);
-    paged_attn_kernel<KIND, NB><<<grid, 256, lds, st>>>(a);
+    paged_attn_kernel<KIND, NB, WHOLE><<<grid, 256, lds, st>>>(a);
     if (a.per_unit) return;
     const int64_t units = a.head_spaces * a.batch;
     if (units * 8 <= a.groups)
@@ -970,17 +1299,17 @@ void launch(const AttnArgs& a, hipStream_t st) {
         paged_attn_join_kernel<32 * NB><<<dim3((unsigned)(a.meta_by_unit ? units : a.groups)), 256, 0, st>>>(a);
 }
 
-template <int KIND>
+template <int KIND, bool WHOLE = false>
 void launch_kind(const AttnArgs& a, int head_dim, hipStream_t st) {
     switch (head_dim / 32) {
-        case 1: launch<KIND, 1>(a, st); break;
-        case 2: launch<KIND, 2>(a, st); break;
-        case 3: launch<KIND, 3>(a, st); break;
-        case 4: launch<KIND, 4>(a, st); break;
-        case 5: launch<KIND, 5>(a, st); break;
-        case 6: launch<KIND, 6>(a, st); break;
-        case 7: launch<KIND, 7>(a, st); break;
-        case 8: launch<KIND, 8>(a, st); break;
+        case 1: launch<KIND, 1, WHOLE>(a, st); break;
+        case 2: launch<KIND, 2, WHOLE>(a, st); break;
+        case 3: launch<KIND, 3, WHOLE>(a, st); break;
+        case 4: launch<KIND, 4, WHOLE>(a, st); break;
+        case 5: launch<KIND, 5, WHOLE>(a, st); break;
+        case 6: launch<KIND, 6, WHOLE>(a, st); break;
+        case 7: launch<KIND, 7, WHOLE>(a, st); break;
+        case 8: launch<KIND, 8, WHOLE>(a, st); break;
     }
 }
 
@@ -1022,6 +1351,8 @@ void launch_paged_attention(const AttnArgs& a, int head_dim, hipStream_t st) {
         launch_kind<KV_F16>(a, head_dim, st);
     else if (a.kind == KV_BF16)
         launch_kind<KV_BF16>(a, head_dim, st);
+    else if (a.kind == KV_MX4 && a.page_size >= 16 && a.slot_units < (1u << 23) && a.scale_slot < (1 << 27))
+        launch_kind<KV_MX4, true>(a, head_dim, st);  // 16 rows' offsets are 31 bits
     else if (a.kind == KV_MX4)
         launch_kind<KV_MX4>(a, head_dim, st);
     else

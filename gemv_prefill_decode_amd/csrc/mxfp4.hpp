@@ -27,11 +27,10 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t bits) {
     const uint32_t e = bits >> 23;
     return e == 255 ? 255u : e > 2 ? e - 2 : 0u;
 }
-// 2^(byte - 127) as f32; 255: an infinity, which the scaled conversions take as NaN.
-__device__ __forceinline__ float mx_scale(uint32_t byte) {
-    const uint32_t b = byte << 23;
-    return __builtin_bit_cast(float, b ? b : 0x00400000u);
-}
+// A scale byte as the scaled conversions take it: they read an f32's exponent
+// field alone (compared over all 256 with other signs and mantissas), 0 being
+// 2^-127 and 255 NaN.
+__device__ __forceinline__ float mx_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 // The codes of four values over their block's scale, element 0 lowest.
 __device__ __forceinline__ uint32_t mx_codes4(f32x4 x, uint32_t byte) {
     const float s = mx_scale(byte);
