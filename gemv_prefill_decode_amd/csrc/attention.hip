@@ -517,29 +517,51 @@ struct Segment {
 };
 
 // ------------------------------------------------------------------ MXFP4 rows
-// The N scale bytes of an MXFP4 row, byte b in bits 8b of the pair.
+// Two bytes or one in the low end of a register, what lies above them left open: an
+// extension to 32 bits that the compiler puts apart from the load waits for it.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint32_t low_bytes(uint16_t v) {
+    const u16x2 x = {v, 0};
+    return __builtin_bit_cast(uint32_t, __builtin_shufflevector(x, x, 0, -1));
+}
+__device__ __forceinline__ uint32_t low_bytes(uint8_t v) {
+    const u8x4 x = {v, 0, 0, 0};
+    return __builtin_bit_cast(uint32_t, __builtin_shufflevector(x, x, 0, -1, -1, -1));
+}
+// The N scale bytes of an MXFP4 row: the first in x and the last in y, so many
+// as one load takes (those between are in both), and block b's place in them.
 template <int N>
 __device__ __forceinline__ u32x2 scale_bytes(const uint8_t* p) {
-    uint32_t lo = 0, hi = 0;
-    if constexpr (N >= 4) __builtin_memcpy(&lo, p, 4);
-    if constexpr (N == 8) __builtin_memcpy(&hi, p + 4, 4);
-    constexpr int AT = N & 4, REST = N & 3;
-    uint32_t rest = 0;
-    if constexpr (REST >= 2) {
+    uint32_t x = 0, y = 0;
+    if constexpr (N >= 4) {
+        __builtin_memcpy(&x, p, 4);
+        if constexpr (N > 4) __builtin_memcpy(&y, p + N - 4, 4);
+    } else if constexpr (N > 1) {
         uint16_t h;
-        __builtin_memcpy(&h, p + AT, 2);
-        rest = h;
+        __builtin_memcpy(&h, p, 2);
+        x = low_bytes(h);
+        if constexpr (N > 2) {
+            __builtin_memcpy(&h, p + 1, 2);
+            y = low_bytes(h);
+        }
+    } else {
+        x = low_bytes(*p);
     }
-    if constexpr (REST & 1) rest |= (uint32_t)p[AT + REST - 1] << (8 * (REST - 1));
-    if constexpr (REST > 0 && AT) hi = rest;
-    if constexpr (REST > 0 && !AT) lo = rest;
-    return u32x2{lo, hi};
+    return u32x2{x, y};
 }
-// Scale of block b as the scaled conversions take it: byte b in the exponent's
+template <int N>
+__device__ __forceinline__ bool scale_in_y(int b) {
+    return b >= (N >= 4 ? 4 : 2);
+}
+template <int N>
+__device__ __forceinline__ int scale_bit(int b) {
+    return 8 * (scale_in_y<N>(b) ? b - (N >= 4 ? N - 4 : 1) : b);
+}
+// A block's scale as the scaled conversions take it: its byte in the exponent's
 // place, the rest does not matter (mxfp4.hpp).
-__device__ __forceinline__ float block_scale(u32x2 w, int b) {
-    const uint32_t v = b & 4 ? w.y : w.x;
-    return fbits(__builtin_amdgcn_alignbit(v, v, (uint32_t)(8 * (b & 3) + 9) & 31u));
+__device__ __forceinline__ float block_scale(uint32_t w, int bit) {
+    return fbits(__builtin_amdgcn_alignbit(w, w, (uint32_t)(bit + 9) & 31u));
 }
 // Codes 2 BYTE and 2 BYTE + 1 of a dword as bf16, exact.
 template <int BYTE>
@@ -647,18 +669,23 @@ struct SegmentMx {
     // Rows of one tile: the lane's share.
     struct Tile {
         u32x4 k[2][NG];      // of row i of each half, block 4 g + c
-        uint32_t ks[2][NG];  // and its scale byte
+        u32x2 ks[2];         // and the row's scales
         uint32_t v[8][VW];   // rows tok_of(j)
         u32x2 vs;            // scales of row tok_of(i % 8)
     };
     // block of group g in lane c; those past the last are read as the last, and q's are zero
     static __device__ __forceinline__ int block(int g, int c) { return 4 * g + c < NB ? 4 * g + c : NB - 1; }
-    static __device__ __forceinline__ void load_k_row(u32x4 (&k)[NG], uint32_t (&ks)[NG], const char* row, const uint8_t* scales, int c) {
+    // a key row's and a value row's share: a row at `at` from base (one 32-bit sum: the load adds it to a
+    // scalar base by itself).  Of values dwords, the lane's or those that its half or quarter of one lies in.
+    static __device__ __forceinline__ void load_k_row(u32x4 (&k)[NG], const char* base, uint32_t at, int c) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            k[g] = *(const u32x4*)(row + 16 * block(g, c));
-            ks[g] = scales[block(g, c)];
-        }
+        for (int g = 0; g < NG; ++g) k[g] = *(const u32x4*)(base + (at + 16u * (uint32_t)block(g, c)));
+    }
+    static __device__ __forceinline__ void load_v_row(uint32_t (&v)[VW], const char* base, uint32_t at, int i) {
+#pragma unroll
+        for (int g = 0; g < N8; ++g) v[g] = *(const uint32_t*)(base + (at + 64u * g + 4u * (uint32_t)i));
+        if constexpr (N4) v[N8] = *(const uint32_t*)(base + (at + 64u * N8 + 4u * (uint32_t)(i / 2)));
+        if constexpr (N2) v[N8 + N4] = *(const uint32_t*)(base + (at + 64u * N8 + 32u * N4 + 4u * (uint32_t)(i / 4)));
     }
 
     __device__ __forceinline__ void run(const AttnArgs& a, int b, int len, int kvh, int head0, int rows, int t, int n) {
@@ -681,12 +708,6 @@ struct SegmentMx {
         const int mask = a.page_size - 1;
 
         auto tok_of = [&](int j) { return (j < 4 ? 0 : 12) + 4 * c + j; };  // token of the lane's k index j
-        auto load_v_row = [&](uint32_t (&v)[VW], const char* row) {
-#pragma unroll
-            for (int g = 0; g < N8; ++g) v[g] = *(const uint32_t*)(row + 64 * g + 4 * i);
-            if constexpr (N4) v[N8] = *(const uint16_t*)(row + 64 * N8 + 2 * i);
-            if constexpr (N2) v[N8 + N4] = *(const uint8_t*)(row + 64 * N8 + 32 * N4 + i);
-        };
         // page ids of a tile: of its halves' first tokens (even and odd lanes), or of the lane's rows
         struct Ids {
             int id[3];
@@ -722,61 +743,56 @@ struct SegmentMx {
             *off = pg * a.page_units + slot * a.slot_units;
             *soff = (int64_t)pg * a.scale_page + (int64_t)slot * a.scale_slot;
         };
+        uint32_t k_at = (uint32_t)i * sb, v_at = (uint32_t)(4 * c) * sb, ks_at = (uint32_t)i * ss;
         auto load_keys = [&](Tile& x, const Ids& p, int tt) {
+            asm volatile("" : "+v"(k_at), "+v"(ks_at));  // extended to 64 bits ahead, they would not be added by the loads
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 int64_t soff;
                 if constexpr (WHOLE) {  // rows behind the last token are masked by their scores
                     int64_t off;
                     half_rows(p, tt, h, &off, &soff);
-                    load_k_row(x.k[h], x.ks[h], kb + off + (uint32_t)i * sb, ksb + soff + (uint32_t)i * ss, c);
+                    load_k_row(x.k[h], kb + off, k_at, c);
+                    x.ks[h] = scale_bytes<NB>(ksb + soff + ks_at);
                 } else {
                     uint32_t off;
                     one_row(p.id[h], clamp_tok(TILE * tt + 16 * h + i), &off, &soff);
-                    load_k_row(x.k[h], x.ks[h], kb + ((uint64_t)off << 4), ksb + soff, c);
+                    load_k_row(x.k[h], kb + ((uint64_t)off << 4), 0, c);
+                    x.ks[h] = scale_bytes<NB>(ksb + soff);
                 }
             }
         };
         auto load_values = [&](Tile& x, const Ids& p, int tt) {
+            asm volatile("" : "+v"(v_at));
             if constexpr (WHOLE) {
                 int64_t off[2], soff[2];
                 half_rows(p, tt, 0, &off[0], &soff[0]);
                 half_rows(p, tt, 1, &off[1], &soff[1]);
-                const int mine = (i >> 2) & 1, left = len - TILE * tt - 1;
-                if (left >= TILE - 1) {
-                    x.vs = scale_bytes<NB>(vsb + (mine ? soff[1] : soff[0]) + (uint32_t)(4 * c + (i & 3)) * ss);
+                // (rows behind the last token get a scale of 0, and p is 0 there)
+                x.vs = scale_bytes<NB>(vsb + ((i & 4) ? soff[1] : soff[0]) + (uint32_t)(4 * c + (i & 3)) * ss);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) load_v_row(x.v[j], vb + off[j >> 2] + (uint32_t)(j & 3) * sb + (uint32_t)(4 * c) * sb);
-                } else {
-                    // row r of half h; rows behind the last are read as the last (in half 1's place, where
-                    // it has none, lie the last token's 16)
-                    auto row = [&](int r, int h) {
-                        const int most = left - 16 * h;
-                        return (uint32_t)(most < 0 ? left & 15 : r < most ? r : most);
-                    };
-                    x.vs = scale_bytes<NB>(vsb + (mine ? soff[1] : soff[0]) + row(4 * c + (i & 3), mine) * ss);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) load_v_row(x.v[j], vb + off[j >> 2] + row(4 * c + (j & 3), j >> 2) * sb);
-                }
+                for (int j = 0; j < 8; ++j) load_v_row(x.v[j], vb + off[j >> 2] + (uint32_t)(j & 3) * sb, v_at, i);
             } else {
                 uint32_t off;
                 int64_t soff;
                 one_row(p.id[2], clamp_tok(TILE * tt + tok_of(i & 7)), &off, &soff);
                 x.vs = scale_bytes<NB>(vsb + soff);
-                auto each_row = [&](auto j) { load_v_row(x.v[j], vb + ((uint64_t)row_lane<j>(off) << 4)); };
+                auto each_row = [&](auto j) { load_v_row(x.v[j], vb + ((uint64_t)row_lane<j>(off) << 4), 0, i); };
                 for_eight(each_row);
             }
         };
 
         Tile tile[TILES];
         Ids ids = page_ids(t);
-        // tile `it`, if there is one, and the page ids of the one after
+        // Tile `it` and the page ids of the one after, these first: a wait for them leaves the tile's
+        // rows on their way.  Past the end the last tile once more: without a branch, the waits for a
+        // tile know how many loads came after its own.
+        auto later = [&](int it) { return t + (it < n ? it : n - 1); };
         auto fetch = [&](Tile& x, int it) {
-            if (it < n) {
-                load_keys(x, ids, t + it);
-                load_values(x, ids, t + it);
-                if (it + 1 < n) ids = page_ids(t + it + 1);
-            }
+            const Ids mine = ids;
+            ids = page_ids(later(it + 1));
+            load_keys(x, mine, later(it));
+            load_values(x, mine, later(it));
         };
 #pragma unroll
         for (int z = 0; z < (TILES > 1 ? TILES - 1 : 1); ++z) fetch(tile[z], z);
@@ -831,9 +847,13 @@ struct SegmentMx {
             f32x4 raw[2] = {};
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
+                uint32_t ks[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    ks[h] = (scale_in_y<NB>(block(g, c)) ? x.ks[h].y : x.ks[h].x) >> scale_bit<NB>(block(g, c));
                 auto part = [&](auto p) {
-                    raw[0] = mfma_parts<p & 3>(x.k[0][g], x.ks[0][g], qp[g][p], qe[g][p / 4], raw[0]);
-                    raw[1] = mfma_parts<p & 3>(x.k[1][g], x.ks[1][g], qp[g][p], qe[g][p / 4], raw[1]);
+                    raw[0] = mfma_parts<p & 3>(x.k[0][g], ks[0], qp[g][p], qe[g][p / 4], raw[0]);
+                    raw[1] = mfma_parts<p & 3>(x.k[1][g], ks[1], qp[g][p], qe[g][p / 4], raw[1]);
                 };
                 part(std::integral_constant<int, 0>{});
                 part(std::integral_constant<int, 1>{});
@@ -849,8 +869,10 @@ struct SegmentMx {
             const int left = len - TILE * tt;
             if (left < TILE) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 8; ++j) {
+                    asm volatile("" : "+v"(s[j]));  // stays a branch
                     if (tok_of(j) >= left) s[j] = -INFINITY;
+                }
             }
             float top = s[0];
 #pragma unroll
@@ -865,7 +887,7 @@ struct SegmentMx {
             if (left < TILE) {  // (a scale of 0 makes NaN of -inf)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    asm volatile("" : "+v"(p[j]));  // stays a branch
+                    asm volatile("" : "+v"(p[j]));
                     if (tok_of(j) >= left) p[j] = 0.0f;
                 }
             }
@@ -879,22 +901,26 @@ struct SegmentMx {
             u32x4 pp[3];
             cut8(p, pp);
             // the scales of the lane's eight value rows
-            u32x2 vs[8];
+            u32x2 vs[8], mine = x.vs;
+            if (WHOLE && left < TILE && tok_of(i & 7) >= left) mine = u32x2{0, 0};
             auto spread = [&](auto j) {
-                vs[j].x = row_lane<j>(x.vs.x);
-                vs[j].y = NB > 4 ? row_lane<j>(x.vs.y) : 0u;
+                vs[j].x = row_lane<j>(mine.x);
+                vs[j].y = NB == 3 || NB > 4 ? row_lane<j>(mine.y) : 0u;
             };
             for_eight(spread);
             // dword w of the value rows: N of its bytes, two operands each, from operand o on, of block blk
             auto dword = [&](auto n, int w, int o, int blk) {
+                uint32_t v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = n == 4 ? x.v[j][w] : x.v[j][w] >> (n == 2 ? 16 * (i & 1) : 8 * (i & 3));
                 float scale[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) scale[j] = block_scale(vs[j], blk);
+                for (int j = 0; j < 8; ++j) scale[j] = block_scale(scale_in_y<NB>(blk) ? vs[j].y : vs[j].x, scale_bit<NB>(blk));
                 auto byte = [&](auto at) {
                     u32x4 lo, hi;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t y = mx_bf16x2<at>(x.v[2 * j][w], scale[2 * j]), z = mx_bf16x2<at>(x.v[2 * j + 1][w], scale[2 * j + 1]);
+                        const uint32_t y = mx_bf16x2<at>(v[2 * j], scale[2 * j]), z = mx_bf16x2<at>(v[2 * j + 1], scale[2 * j + 1]);
                         lo[j] = __builtin_amdgcn_perm(z, y, 0x05040100u);
                         hi[j] = __builtin_amdgcn_perm(z, y, 0x07060302u);
                     }
@@ -919,23 +945,24 @@ struct SegmentMx {
         // The rows of TILES - 1 tiles are on their way behind the arithmetic of one; where there is room
         // for one tile, its registers take the next one's as soon as they are read.
         if constexpr (TILES > 1) {
-            for (int it = 0; it < n; it += TILES)
+            int it = 0;
+            for (; it + TILES <= n; it += TILES)
 #pragma unroll
-                for (int z = 0; z < TILES; ++z)
-                    if (it + z < n) {
-                        fetch(tile[(z + TILES - 1) % TILES], it + z + TILES - 1);
-                        work(tile[z], t + it + z, [] {});
-                    }
+                for (int z = 0; z < TILES; ++z) {
+                    fetch(tile[(z + TILES - 1) % TILES], it + z + TILES - 1);
+                    work(tile[z], t + it + z, [] {});
+                }
+#pragma unroll
+            for (int z = 0; z < TILES - 1; ++z)
+                if (it + z < n) work(tile[z], t + it + z, [] {});
         } else {
             for (int it = 0; it < n; ++it) {
                 const Ids mine = ids;
                 work(tile[0], t + it, [&] {
-                    if (it + 1 < n) {
-                        load_keys(tile[0], mine, t + it + 1);
-                        if (it + 2 < n) ids = page_ids(t + it + 2);
-                    }
+                    ids = page_ids(later(it + 2));
+                    load_keys(tile[0], mine, later(it + 1));
                 });
-                if (it + 1 < n) load_values(tile[0], mine, t + it + 1);
+                load_values(tile[0], mine, later(it + 1));
             }
         }
         if (__any(bad)) l = NAN;
