@@ -340,7 +340,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_mx_tile_kernel(const M
     // a token; the k groups' sums are added in order.
     wait(std::integral_constant<int, 0>{});
     constexpr int ROW = 4 * BM + 16, PLACE = 16 * WN * ROW;  // 16 bytes apart: the tokens of a wave's write in different banks
-    static_assert(2 * PLACE <= T::LDS, "outputs");
+    static_assert(2 * PLACE + 4 * BN <= T::LDS, "outputs");
+    // the tokens' scales too: a load of one would wait for the stores before it
+    float* const tok_scale = (float*)(all_lds + 2 * PLACE);
+    for (int t = threadIdx.x; t < BN; t += T::THREADS * KG) tok_scale[t] = a.s && n0 + t < a.n ? a.s[n0 + t] : 1.0f;
     const bool wide = (a.m & 3) == 0 && (a.ldd & 3) == 0 && ((uintptr_t)a.dst & 15) == 0;
     auto write = [&](auto at) {
         constexpr int y = at;
@@ -351,13 +354,14 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_mx_tile_kernel(const M
 #pragma unroll 1
         for (int e = threadIdx.x; e < 16 * WN * (BM / 4); e += T::THREADS * KG) {
             const int t = e / (BM / 4), r = 4 * (e % (BM / 4));
-            const int64_t tok = n0 + (t / 16) * (16 * NJ) + 16 * y + t % 16, row = m0 + r;
+            const int of_tile = (t / 16) * (16 * NJ) + 16 * y + t % 16;
+            const int64_t tok = n0 + of_tile, row = m0 + r;
             if (tok >= a.n || row >= a.m) continue;
             const uint8_t* sum = all_lds + (y & 1) * PLACE + t * ROW + 4 * r;
             f32x4 v = *(const f32x4*)sum;
 #pragma unroll
             for (int z = 1; z < KG; ++z) v += *(const f32x4*)(sum + z * T::LDS);
-            if (a.s) v *= a.s[tok];
+            v *= tok_scale[of_tile];
             float* d = a.dst + tok * a.ldd + row;
             if (wide) {
                 __builtin_nontemporal_store(v, (f32x4*)d);
