@@ -637,7 +637,7 @@ __device__ __forceinline__ f32x4 mfma_parts(u32x4 k, uint32_t ks, u32x6 q, uint3
 //
 // Scores: v_mfma_scale_f32_16x16x128_f8f6f4 takes the key rows' codes and scales
 // as they are, lane (c, i) block 4 g + c of row i, against q in six E2M3 parts, each
-// with a scale per block: their sum is x up to 2^-30 of its block's largest.  (Key
+// with a scale per block: their sum is x up to 2^-29 of its block's largest.  (Key
 // codes made bf16 against q in three bf16 parts: 24 matrix instructions for 12 at a
 // head of 128 and 34 more of the vector ALUs, which are the busier.  131071 tokens of
 // 8 heads of 128 took 51.0 us that way, 48.2 this; 61 ragged sequences of up to 16384

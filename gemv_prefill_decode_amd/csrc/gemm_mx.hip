@@ -425,12 +425,20 @@ constexpr Kernel KERNELS[] = {
 int gemm_mxfp4_kernels() { return (int)(sizeof(KERNELS) / sizeof(KERNELS[0])); }
 
 void launch_gemm_mxfp4(const MxGemmArgs& a, int forced, int num_cu, hipStream_t st) {
-    if (forced >= 0 && !(KERNELS[forced].even && a.k % 64 != 0)) return KERNELS[forced].launch(a, st);
+    auto work_groups_of = [&](const Kernel& x) {
+        return (int64_t)((a.m + x.rows - 1) / x.rows) * ((a.n + x.tokens - 1) / x.tokens);
+    };
+    // a launch has fewer than 2^32 threads, a grid's second axis fewer than 2^16 work groups
+    // (2^37 outputs, the most there are, are 2^21 tiles of 256 x 256, and 2^13 more at the ends)
+    auto runs = [&](const Kernel& x) {
+        return !(x.even && a.k % 64 != 0) && work_groups_of(x) <= 1 << 22 && (a.n + x.tokens - 1) / x.tokens < 1 << 16;
+    };
+    if (forced >= 0 && runs(KERNELS[forced])) return KERNELS[forced].launch(a, st);
     const Kernel* best = nullptr;
     double least = 0;
     for (const Kernel& x : KERNELS) {
-        if (x.even && a.k % 64 != 0) continue;
-        const int64_t work_groups = (int64_t)((a.m + x.rows - 1) / x.rows) * ((a.n + x.tokens - 1) / x.tokens);
+        if (!runs(x)) continue;
+        const int64_t work_groups = work_groups_of(x);
         const int64_t rounds = (work_groups + (int64_t)num_cu * x.per_cu - 1) / ((int64_t)num_cu * x.per_cu);
         const int groups = ((a.k + x.pass - 1) / x.pass + x.k_groups - 1) / x.k_groups;
         const double each = (double)work_groups / num_cu;

@@ -320,7 +320,7 @@ int gemm_impl(float* dst, int64_t ldd, const void* w, const float* x, int64_t ld
 
 // Largest sizes of an MXFP4 product: 256 rows of k/2 bytes below 2^31, 2^20
 // tokens.
-constexpr int64_t MX_K_MAX = (int64_t)1 << 23, MX_N_MAX = (int64_t)1 << 20;
+constexpr int64_t MX_K_MAX = (int64_t)1 << 23, MX_N_MAX = (int64_t)1 << 20, MX_M_MAX = (int64_t)1 << 26;
 
 // ------------------------------------------------------------------ decode step
 // Tokens of a cache or a table row, table entries and rows of a step: int32
@@ -1104,8 +1104,8 @@ int qmm_gemm_mxfp4(float* dst, int64_t ldd, const uint8_t* wq, const uint8_t* we
     if (k % 32 != 0) return QMM_ERR_K_ALIGN;
     if (!aligned(wq, 16) || !aligned(xq, 16) || !aligned(we, 4) || !aligned(xe, 4) || !aligned(dst, 4) || !aligned(x_scale, 4))
         return QMM_ERR_ALIGN;
-    // a tile's rows are addressed by 31-bit byte offsets, its tokens by a grid's second axis
-    if (k > MX_K_MAX || m > INT_MAX - 256 || n > MX_N_MAX) return QMM_ERR_RANGE;
+    // a tile's rows are addressed by 31-bit byte offsets; work groups are at most 2^22
+    if (k > MX_K_MAX || m > MX_M_MAX || n > MX_N_MAX || m * n > (int64_t)1 << 37) return QMM_ERR_RANGE;
     int64_t span;
     if (!mul_ok(n, ldd, &span) || span > INT64_MAX / 4) return QMM_ERR_SHAPE;
     const Span ins[] = {{wq, m * k / 2}, {we, m * k / 32}, {xq, n * k / 2}, {xe, n * k / 32}, {x_scale, x_scale ? n * 4 : 0}};

@@ -554,11 +554,13 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * or value makes the outputs that it enters non-finite, except that a score
  * of -inf may count as a weight of zero; the same holds for scores beyond the
  * f32 range.
- * f32 arithmetic: f32 operands enter the matrix cores as two f16 (a bf16 or
- * MXFP4 cache: three bf16) parts, products and sums are f32; the exponential and logarithm are
+ * f32 arithmetic: f32 operands enter the matrix cores as two f16 (three
+ * bf16) parts, products and sums are f32; the exponential and logarithm are
  * the hardware's.  (f16 parts: an element of q is kept to 2^-38 of its head's
- * largest, a weight to 2^-39 of the largest.)  Finite elements and scores
- * give finite outputs.
+ * largest, a weight to 2^-39 of the largest.  An MXFP4 cache: q in six E2M3
+ * parts, an element kept to 2^-29 of the largest of its 32, or 2^-71 of its
+ * head's largest, or 2^-118; weights in three bf16 parts.)  Finite elements
+ * and scores give finite outputs.
  *   out   DEVICE float, rows ldo >= n_q*head_dim apart (a multiple of 4),
  *         16-byte aligned.  lse: DEVICE float[batch*n_q] or NULL.
  *   q     DEVICE float, rows ldq apart (as ldo), 16-byte aligned.
@@ -658,9 +660,11 @@ int qmm_dequantize_mxfp4(float* x, const uint8_t* q, const uint8_t* e, int64_t r
  *   dst    DEVICE float, n rows ldd >= m apart, written; elements between m and
  *          ldd are not.
  *   wq, we DEVICE codes and scales of m rows of k; xq, xe those of n rows.  Codes
- *          16-byte aligned, scales 4-byte.
+ *          16-byte aligned, scales 4-byte (the 4 bytes that hold the last scale
+ *          are read whole).
  *   x_scale  DEVICE float[n], or NULL: qmm_add_rmsnorm_mxfp4's factors.
- *   k      a multiple of 32, at most 2^23; n at most 2^20 (QMM_ERR_RANGE).
+ *   k      a multiple of 32, at most 2^23; m at most 2^26, n 2^20, m*n 2^37
+ *          (QMM_ERR_RANGE).
  * A cost model fitted to MI355X measurements picks one of 11 kernels (tiles
  * from 16 x 16 to 256 x 256, with or without groups of waves that share a sum).
  * The sums' order depends on the sizes alone: identical calls are bit-identical.

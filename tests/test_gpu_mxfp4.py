@@ -158,6 +158,24 @@ def test_gemm_every_kernel(kernel, monkeypatch):
             assert np.isnan(got[:, m // 2]).all() and np.isfinite(np.delete(got, m // 2, 1)).all()
 
 
+@pytest.mark.parametrize("m,k,n", [(16, 64, 1 << 20), (7, 32, (1 << 20) - 3), ((1 << 22) + 5, 64, 1), ((1 << 20) + 16, 32, 17)])
+def test_gemm_many_rows(m, k, n):
+    """As many tokens as there may be, and as many rows as one kind of tile would need a grid too
+    large for.  All products are multiples of 1/4 below 36, their sums exact."""
+    torch, qmm = _torch(), _qmm()
+    gh.note(f"gemm_mxfp4 {m}x{k} n={n}")
+    torch.manual_seed(m % 97)
+    (w, we), (x, xe) = (tuple((torch.randint(0, 256, (r, k // 2), dtype=torch.uint8, device="cuda"),
+                               torch.full((r, k // 32), 127, dtype=torch.uint8, device="cuda"))) for r in (m, n))
+    out = torch.full((n, m), math.nan, device="cuda")
+    qmm.gemm_mxfp4(w, we, x, xe, out=out)
+    for i in torch.randint(0, n, (8,)).tolist() + [0, n - 1]:
+        assert torch.equal(out[i], (qmm.dequantize_mxfp4(w, we) * qmm.dequantize_mxfp4(x[i:i + 1], xe[i:i + 1])).sum(1))
+    wf = qmm.dequantize_mxfp4(w, we)
+    for i in torch.randint(0, m, (8,)).tolist() + [0, m - 1]:
+        assert torch.equal(out[:, i], (qmm.dequantize_mxfp4(x, xe) * wf[i]).sum(1))
+
+
 def test_gemm_malformed_kernel_choice(monkeypatch):
     qmm = _qmm()
     args = [_dev(np.zeros(s, np.uint8)) for s in ((2, 16), (2, 1), (3, 16), (3, 1))]
@@ -381,6 +399,33 @@ def test_attention_scores_and_scales_far_apart():
     _check(_case([300, 90], 2, 4, 128, 16, scales=(100, 135), q_mul=0.05))
     _check(_case([300, 90], 2, 4, 64, 16, scales=(127, 131), q_mul=20.0))
     _check(_case([64], 1, 2, 96, 16, scales=(0, 40)))
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("scale", [-0.25, 0.0, 2.0 ** -30])
+def test_attention_query_blocks_far_apart(d, scale):
+    """A query's block of 32 is kept to 2^-29 of its largest element, whatever the other blocks hold: a
+    score is off by up to 2^-29 M sum|k| per block, M its largest |q|, which the oracle's (d + 12) 2^-24
+    sum|q k| holds as long as M sum|k| is below 2^5 (d + 12) sum|q k|, here by far."""
+    for page, tail in ((16, 37), (4, 6)):
+        c = _case([tail, 0, 96 + tail], 2, 3, d, page, scales=(120, 127), scale=scale)
+        c["q"] *= np.repeat(2.0 ** np.random.default_rng(d).integers(-25, 3, (3, 6, d // 32)), 32, axis=-1).astype(np.float32)
+        _check(c)
+
+
+def test_attention_query_that_is_not_finite():
+    torch, qmm = _torch(), _qmm()
+    for d in (32, 128, 160):
+        c = _case([70, 40, 33], 2, 4, d, 16)
+        args = lambda q: (_dev(q), c["cache"], _dev(c["table"]), torch.tensor(c["lens"], dtype=torch.int32, device="cuda"))  # noqa: E731
+        good = qmm.paged_attention(*args(c["q"]))
+        assert torch.isfinite(good).all()
+        bad = c["q"].copy()
+        bad[0, 1, 5], bad[1, 6, d - 1], bad[2, 0, 0] = np.inf, np.nan, -np.inf
+        out = qmm.paged_attention(*args(bad))
+        hit = torch.zeros(3, 8, dtype=torch.bool, device="cuda")
+        hit[0, 1] = hit[1, 6] = hit[2, 0] = True
+        assert not torch.isfinite(out[hit]).any() and torch.equal(out[~hit], good[~hit])
 
 
 def test_attention_bad_data():

@@ -64,6 +64,7 @@ def test_gemm_refusals():
     assert f(wq=_off(P[1], 8)) == f(xq=_off(P[3], 8)) == f(we=_off(P[2], 2)) == f(xe=_off(P[4], 1)) == ALIGN
     assert f(dst=_off(P[0], 2)) == f(s=_off(P[5], 2)) == ALIGN
     assert f(k=(1 << 23) + 32) == f(m=1 << 31, ldd=1 << 31) == f(n=(1 << 20) + 1) == RANGE
+    assert f(m=(1 << 26) + 1, ldd=1 << 27) == f(m=1 << 26, ldd=1 << 26, n=(1 << 11) + 1) == RANGE
     for other in (P[1], P[2], P[3], P[4], P[5]):
         assert f(dst=other) == f(dst=_off(other, -4)) == ALIAS
     assert f(dst=_off(P[1], 48 * 48 - 4)) == f(dst=_off(P[4], 12)) == ALIAS
