@@ -10,13 +10,15 @@
 // Bounds and measured times (MI355X, operands in HBM).  Few tokens: the weights'
 // bytes, 14336 x 4096 with 16 tokens (32 MB) 7.6 us, 4.2 TB/s; or latency, 4608 x
 // 1024 with one 3.2 us, 1024 x 4608 with 512 6.8 us.  Many, 14336 x 4096 with 2048:
-// 78.6 us, 3.06 PFLOP/s, where the matrix instructions alone take 44 to 51 us (the
+// 76.0 us, 3.16 PFLOP/s, where the matrix instructions alone take 44 to 51 us (the
 // clock falls with the data), the loads into LDS alone 54 us (L2 gives about 15 TB/s
-// of whole lines) and the outputs, behind which no loads go on, 13 to 19 us.
+// of whole lines) and the outputs, behind which no loads go on, 13 to 19 us; operands'
+// reads from LDS and the loads' writes keep it as busy as the matrix cores are.
 // In turn: operands straight from memory 656 us; 128 x 128 tiles through LDS 126;
 // scales as 16 bytes a row 98; whole lines of outputs past the caches 90; lines of
 // 128 bytes with operands read ahead 85; outputs through LDS and 256 x 256 tiles 79.5;
-// the tokens' factors out of the stores' way 78.6.  Rings of more and shorter stages
+// the tokens' factors out of the stores' way 78.6; the tokens' loads ahead of the
+// stage's end 76.0.  Rings of more and shorter stages
 // (64 bytes a row) lost more on half lines than they hid; loads that warm L2 ahead
 // gained nothing.
 #include <type_traits>
@@ -184,10 +186,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_mx_tile_kernel(const M
 
     // A load takes 8 rows of eight chunks.  (Where the loads do not divide, the last waves
     // load the last rows once more.)
-    auto issue = [&](int s, int slot) {
+    auto issue = [&](int s, int slot, auto first, auto last) {
         uint8_t* st = lds + slot * T::STAGE;
 #pragma unroll
-        for (int u = 0; u < T::D; ++u) {
+        for (int u = first; u < last; ++u) {
             const int l = T::D * T::WAVES == T::LOADS || u * T::WAVES + w < T::LOADS ? u * T::WAVES + w : T::LOADS - 1;
             const bool of_w = l < BM / 8;
             const int blk = 8 * stage_of(s) + ((lane & 7) ^ (4 * (l & 1) + (lane >> 4)));
@@ -273,13 +275,22 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_mx_tile_kernel(const M
         asm volatile("" ::: "memory");
     };
 
+    // Large tiles: the tokens' share of a stage is in registers long before the weights', and its place
+    // takes loads then: there are some on their way all the time, not only after the stage's end.
+    constexpr int MID = 6, LAST = 2 * RI - PF;
+    constexpr bool SPLIT = MID + 2 < LAST;
+    constexpr int OF_W = SPLIT ? BM / 8 / T::WAVES : T::D;  // a wave's loads of weights
+    static_assert(!SPLIT || (BM / 8 % T::WAVES == 0 && BN / 8 % T::WAVES == 0 && MID < RI && NJ <= 4), "loads");
+    const std::integral_constant<int, 0> none{};
+    const std::integral_constant<int, OF_W> of_w{};
+    const std::integral_constant<int, T::D> all{};
     load_scales(0);
 #pragma unroll
-    for (int p = 0; p < NR - 1; ++p) issue(p, p);
+    for (int p = 0; p < NR - 1; ++p) issue(p, p, none, all);
     store_scales(0);
     wait(std::integral_constant<int, (NR - 2) * T::D>{});
     if constexpr (RI <= 4) load_scales(1);
-    issue(NR - 1, NR - 1);
+    issue(NR - 1, NR - 1, none, all);
 #pragma unroll
     for (int q = 0; q < PF; ++q) fa[q] = operand(lds, arow + 16 * (q % RI), q / RI);
 #pragma unroll
@@ -292,7 +303,6 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_mx_tile_kernel(const M
     // tile q + PF read behind them.  Before tile LAST, where the stage's last operands are in
     // registers, one barrier: the next stage is whole, and this one's place takes the loads of the
     // one after.
-    constexpr int LAST = 2 * RI - PF;
     int place = 0;
     auto stage = [&](int s, auto odd_stage) {
         constexpr int O = odd_stage;
@@ -308,11 +318,24 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void gemm_mx_tile_kernel(const M
             constexpr int q = at, h = q / RI, x = q % RI;
             const u32x4 f = fa[q % PF];
             if constexpr (q < LAST) fa[q % PF] = operand(st, arow + 16 * ((q + PF) % RI), (q + PF) / RI);
-            if constexpr (h == 0 && x < NJ) fb_half[x] = operand(st, brow + 16 * x, 1);
+            if constexpr (!SPLIT && h == 0 && x < NJ) fb_half[x] = operand(st, brow + 16 * x, 1);
+            if constexpr (SPLIT && q < (NJ + 1) / 2) {
+                fb_half[2 * q] = operand(st, brow + 32 * q, 1);
+                if constexpr (2 * q + 1 < NJ) fb_half[2 * q + 1] = operand(st, brow + 32 * q + 16, 1);
+            }
+            if constexpr (SPLIT && q == MID) {
+                // LDS answers in order: tile MID - 1 had its operands, read in tile MID - 1 - PF, behind
+                // the tokens' in tiles 0 and 1
+                static_assert(MID - 1 - PF >= (NJ + 1) / 2, "tokens read");
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                issue(s + NR, here, of_w, all);
+            }
             if constexpr (q == LAST) {
-                wait(std::integral_constant<int, (NR - 2) * T::D>{});
+                wait(std::integral_constant<int, (NR - 2) * T::D + T::D - OF_W>{});
                 if constexpr (O == 1 && RI <= 4) load_scales(s / 2 + 2);
-                issue(s + NR, here);
+                issue(s + NR, here, none, of_w);
             }
             if constexpr (q >= LAST) {
                 constexpr int z = q - LAST;
