@@ -893,8 +893,19 @@ struct SegmentMx {
             const float alpha = __builtin_amdgcn_exp2f(m - base);
             m = top;
             float p[8], sum = 0.0f;
+            if (__any(fabsf(base) >= 0x1p20f)) {
+                // a maximum rounded by 1/16 and more: scores rounded alike are at most as large, where
+                // the exact products below may be ahead of it by more than an exponential holds
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], qs, shift));
+                for (int j = 0; j < 8; ++j) {
+                    float x = s[j] * qs;
+                    asm("" : "+v"(x));  // rounded
+                    p[j] = __builtin_amdgcn_exp2f(x - base + pbits);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], qs, shift));
+            }
             if (left < TILE) {  // (a scale of 0 makes NaN of -inf)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {

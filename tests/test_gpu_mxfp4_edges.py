@@ -1,0 +1,52 @@
+"""MXFP4 on the GPU at the edges of what its header allows: attention scales and scores near the ends
+of f32."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import gpu_helpers as gh
+from oracle import mxfp4
+from test_gpu_mxfp4 import _case, _check, _dev, _qmm, _torch
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attention
+def _check_decided(c):
+    """_check, and where a head's largest score is ahead by far more than f32 can be off (2 (d + 12) u
+    of the largest sum of magnitudes, and 200 for the others to weigh nothing) its token's value: a
+    weight and its sum are the same number there, so the output is off by the inverse, a product and
+    the three parts, below 8 u of the value.  Returns how many heads were."""
+    torch, qmm = _torch(), _qmm()
+    _check(c)
+    out = qmm.paged_attention(_dev(c["q"]), c["cache"], _dev(c["table"]),
+                              torch.tensor(c["lens"], dtype=torch.int32, device="cuda"), scale=c["scale"]).cpu().numpy()
+    b, n_q, d = c["q"].shape
+    seen, u = 0, 2.0 ** -24
+    for i in np.flatnonzero(c["lens"]):
+        t = np.arange(c["lens"][i])
+        at = (c["table"][i][t // c["page"]], slice(None), t % c["page"])
+        k, v = (mxfp4.dequantize(c["host"][n][at], c["host"][n + "s"][at]) for n in ("k", "v"))
+        for h in range(n_q):
+            kh, q = k[:, h // (n_q // k.shape[1])], c["q"][i, h].astype(np.float64)
+            s, reach = c["scale"] * (kh @ q), abs(c["scale"]) * (np.abs(kh) @ np.abs(q))
+            order = np.argsort(s)
+            if len(s) == 1 or s[order[-1]] - s[order[-2]] > 2 * (d + 12) * u * reach.max() + 200:
+                want = v[order[-1], h // (n_q // k.shape[1])]
+                assert np.all(np.abs(out[i, h] - want) <= 8 * u * np.abs(want)), (i, h)
+                seen += 1
+    return seen
+
+
+@pytest.mark.parametrize("page", [16, 4])
+@pytest.mark.parametrize("q_mul", [2.0 ** 24, 2.0 ** 29, 2.0 ** 30, 2.0 ** 31, 2.0 ** 33, 2.0 ** 60, 2.0 ** 110])
+def test_attention_any_score(q_mul, page):
+    """A score's own rounding, 64 and more from 2^30 on, does not enter the exponentials."""
+    gh.note(f"attention mxfp4 q*{q_mul} page {page}")
+    seen = 0
+    for lens, tokens in (([70, 1, 0, 33], 0), ([700, 90], 1024), ([1] * 8, 0)):
+        for sign in (1.0, -1.0):
+            seen += _check_decided(_case(lens, 2, 4, 64, page, tokens=tokens, scale=0.125 * sign, q_mul=q_mul))
+    assert seen > 50
