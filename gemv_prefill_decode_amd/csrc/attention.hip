@@ -50,6 +50,7 @@
 // heads of 64, 5.1 us (launch and four dependent loads).  MXFP4: 131071 tokens,
 // 143 MB, 38 us (3.8 TB/s); 61 sequences of up to 16384 tokens, tokens outermost,
 // 376 MB, 98 us (3.8 TB/s).
+#include <cfloat>
 #include <type_traits>
 
 #include "common.hpp"
@@ -148,6 +149,24 @@ __device__ __forceinline__ void ldg(uint32_t (&dst)[N], int at, const char* p, i
     } else {
         dst[at] = ldx<NT, uint16_t>(p);
     }
+}
+
+// The factor that q is multiplied by ahead of products with elements of f32's range: a power of two,
+// as its exponent field, for a head whose largest |q| is top.  2^-12 of the scale's, so that the sum of
+// products passes f32 no sooner than the score, and is lost below it no sooner than the score is
+// nothing; but one that takes top to between 2^-60, where the parts of q are normal numbers, and
+// 2^64, and leaves a factor of less than 2^127 (from there on top to 2^126 at most).
+__device__ __forceinline__ int q_exponent(float top, float scale) {
+    const int te = (int)(ubits(top) >> 23), se = (int)(ubits(scale) >> 23 & 255u);
+    int e = se - 12 < 318 - te ? se - 12 : 318 - te;
+    const int least = 194 - te > se - 126 ? 194 - te : se - 126;
+    e = e < least ? least : e;
+    e = e > 380 - te ? 380 - te : e;
+    return e < 1 ? 1 : e;
+}
+// What takes the sums over q times that factor to log2(e) * score.
+__device__ __forceinline__ float q_scale(int e, float scale) {
+    return __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(scale, 127 - e) * LOG2E, -FLT_MAX, FLT_MAX);
 }
 
 // Eight f32 as f16 (bf16) parts: x = part 0 + part 1 (+ part 2) up to 2^-22
@@ -830,12 +849,11 @@ struct SegmentMx {
                 }
             }
             top = max_c(top);
-            // q's factor: 2^-12, so that the sum of products passes f32 no sooner than the score, but at
-            // least what takes the largest to 2^-60, far from the smallest scale; the scale's sign goes along
-            int e = 194 - (int)(ubits(top) >> 23);
-            e = e < 115 ? 115 : e;
-            const float f = fbits((uint32_t)e << 23 | (a.scale < 0.0f ? 0x80000000u : 0u));
-            qs = fbits((uint32_t)(254 - e) << 23) * fabsf(a.scale) * LOG2E;  // scale * log2(e) may pass f32
+            float scale = a.scale;
+            asm volatile("" : "+v"(scale));  // what is made of it is not kept in scalar registers from unit to unit
+            const int e = q_exponent(top, scale);
+            const float f = fbits((uint32_t)e << 23 | (ubits(scale) & 0x80000000u));  // the scale's sign goes along
+            qs = q_scale(e, fabsf(scale));
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 uint32_t bits = 0;

@@ -559,8 +559,9 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * the hardware's.  (f16 parts: an element of q is kept to 2^-38 of its head's
  * largest, a weight to 2^-39 of the largest.  An MXFP4 cache: q in six E2M3
  * parts, an element kept to 2^-29 of the largest of its 32, or 2^-71 of its
- * head's largest, or 2^-118; weights in three bf16 parts.)  Finite elements
- * and scores give finite outputs.
+ * head's largest; weights in three bf16 parts.)  Finite elements and scores
+ * (scores below 2^127) give finite outputs; with an MXFP4 cache while a head's
+ * largest |q| times |scale| is below 2^252.
  *   out   DEVICE float, rows ldo >= n_q*head_dim apart (a multiple of 4),
  *         16-byte aligned.  lse: DEVICE float[batch*n_q] or NULL.
  *   q     DEVICE float, rows ldq apart (as ldo), 16-byte aligned.

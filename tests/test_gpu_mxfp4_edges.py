@@ -50,3 +50,29 @@ def test_attention_any_score(q_mul, page):
         for sign in (1.0, -1.0):
             seen += _check_decided(_case(lens, 2, 4, 64, page, tokens=tokens, scale=0.125 * sign, q_mul=q_mul))
     assert seen > 50
+
+
+@pytest.mark.parametrize("page", [16, 4])
+@pytest.mark.parametrize("scale,q_mul,scales", [
+    (2.0 ** -30, 2.0 ** 20, (238, 243)),      # sums of products beyond f32, scores of 2^110
+    (-2.0 ** -100, 2.0 ** 60, (240, 245)),
+    (2.0 ** 118, 1.0, (3, 9)),                # scale times 2^12 beyond f32, scores of some units
+    (-3e38, 2.0 ** -3, (0, 3)),
+    (3e38, 1e-37, (122, 129)),
+    (2.0 ** 60, 2.0 ** 50, (10, 20)),
+    (2.0 ** -126, 2.0 ** 100, (140, 150)),
+    (2.0 ** -149, 2.0 ** 120, (145, 155)),
+    (0.0, 2.0 ** 100, (120, 129)),
+    (2.0 ** -126, 2.0 ** 120, (246, 252)),    # products of 2^244
+    (3e38, 2.0 ** 60, (0, 3)),
+])
+def test_attention_any_scale(scale, q_mul, scales, page):
+    """Finite elements and scores give finite outputs whatever the scale."""
+    gh.note(f"attention mxfp4 scale {scale} q*{q_mul} key scales {scales} page {page}")
+    for lens, tokens in (([70, 1, 0, 33], 0), ([700, 90], 1024)):
+        c = _case(lens, 2, 4, 64, page, tokens=tokens, scales=scales, scale=scale, q_mul=q_mul)
+        for name in ("v_scale",):             # values of ordinary size
+            t = getattr(c["cache"], name)
+            t.copy_(_torch().where(t == 255, t, 122 + t % 6))
+            c["host"]["vs"] = t.cpu().numpy()
+        _check_decided(c)
