@@ -398,17 +398,17 @@ struct Segment {
             // q's factor, a power of two: its exponent field
             int e;
             if constexpr (KIND == KV_BF16) {
-                // 2^-12, so that the sum of products passes f32 no sooner than the score, but at
-                // least what takes the largest to 2^-60: its parts are normal numbers
-                e = 194 - (int)(ubits(top) >> 23);
-                e = e < 115 ? 115 : e;
+                float scale = a.scale;
+                asm volatile("" : "+v"(scale));  // what is made of it is not kept in scalar registers from unit to unit
+                e = q_exponent(top, scale);
+                qs = q_scale(e, scale);
             } else {
                 // 2^(13 - floor(log2 top)), kept normal with its inverse
                 e = 267 - (int)(ubits(top) >> 23);
                 e = e > 253 ? 253 : (e < 1 ? 1 : e);
+                qs = fbits((uint32_t)(254 - e) << 23) * a.scale * LOG2E;  // scale * log2(e) may pass f32
             }
             const float f = fbits((uint32_t)e << 23);
-            qs = fbits((uint32_t)(254 - e) << 23) * a.scale * LOG2E;  // scale * log2(e) may pass f32
 #pragma unroll
             for (int s = 0; s < NB; ++s) {
 #pragma unroll

@@ -560,8 +560,9 @@ int qmm_kv_append(const qmm_kv_cache* cache, const float* k, int64_t ldk, const 
  * largest, a weight to 2^-39 of the largest.  An MXFP4 cache: q in six E2M3
  * parts, an element kept to 2^-29 of the largest of its 32, or 2^-71 of its
  * head's largest; weights in three bf16 parts.)  Finite elements and scores
- * (scores below 2^127) give finite outputs; with an MXFP4 cache while a head's
- * largest |q| times |scale| is below 2^252.
+ * (scores below 2^127) give finite outputs while a head's largest |q| times
+ * |scale| is below 2^252 (bf16 and MXFP4) or, times the key's scale too where
+ * rows have one, 2^139 (f16 and 8-bit).
  *   out   DEVICE float, rows ldo >= n_q*head_dim apart (a multiple of 4),
  *         16-byte aligned.  lse: DEVICE float[batch*n_q] or NULL.
  *   q     DEVICE float, rows ldq apart (as ldo), 16-byte aligned.

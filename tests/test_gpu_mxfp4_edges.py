@@ -76,3 +76,18 @@ def test_attention_any_scale(scale, q_mul, scales, page):
             t.copy_(_torch().where(t == 255, t, 122 + t % 6))
             c["host"]["vs"] = t.cpu().numpy()
         _check_decided(c)
+
+
+@pytest.mark.parametrize("scale,q_mul,k_mul", [
+    (2.0 ** -30, 2.0 ** 20, 2.0 ** 115), (-2.0 ** -100, 2.0 ** 60, 2.0 ** 120), (2.0 ** 118, 1.0, 2.0 ** -118),
+    (-3e38, 2.0 ** -3, 2.0 ** -120), (3e38, 1e-37, 0.1), (2.0 ** 60, 2.0 ** 50, 2.0 ** -110),
+    (2.0 ** -149, 2.0 ** 120, 2.0 ** 26), (0.0, 2.0 ** 60, 1.0), (0.125, 2.0 ** 33, 1.0), (-0.125, 2.0 ** 100, 1.0)])
+def test_attention_bf16_any_scale(scale, q_mul, k_mul):
+    """The same of a bfloat16 cache."""
+    import test_gpu_step as of_step
+    gh.note(f"attention bf16 scale {scale} q*{q_mul} k*{k_mul}")
+    for lens, tokens in (([70, 1, 0, 33], 0), ([700, 90], 1024)):
+        c = of_step._case("bf16", lens, 2, 4, 64, 16, tokens=tokens, scale=scale, q_mul=q_mul)
+        k = c["cache"].k
+        k.copy_(_torch().where(_torch().isfinite(k), k.float() * k_mul, k.float()))
+        of_step._check(c)
