@@ -782,6 +782,13 @@ def add_rmsnorm_q8(x, weight, residual=None, eps: float = 1e-5, q=None, d=None, 
 
 
 # ------------------------------------------------------------------ MXFP4
+def _matrix(t, what: str):
+    """The two sizes of an operand (a tensor) that an output is allocated from."""
+    if t.ndim != 2:
+        raise ValueError(f"{what} must be two-dimensional, got {list(t.shape)}")
+    return t.shape
+
+
 def quantize_mxfp4(x, q=None, e=None, stream=None):
     """MXFP4 codes and scales of x (float32, float16 or bfloat16 [rows, k], k a multiple of 32, rows
     any multiple of 16 bytes apart): returns (q uint8 [rows, k/2], e uint8 [rows, k/32]).  A value is
@@ -791,8 +798,9 @@ def quantize_mxfp4(x, q=None, e=None, stream=None):
     dev = step.device(x, "x")
     if q is None or e is None:
         import torch
-        q = _new((x.shape[0], x.shape[-1] // 2), torch.uint8, x, stream) if q is None else q
-        e = _new((x.shape[0], x.shape[-1] // 32), torch.uint8, x, stream) if e is None else e
+        n, k = _matrix(x, "x")
+        q = _new((n, k // 2), torch.uint8, x, stream) if q is None else q
+        e = _new((n, k // 32), torch.uint8, x, stream) if e is None else e
     _run(step.quantize_mxfp4, dev, stream, x, q, e)
     return q, e
 
@@ -804,6 +812,8 @@ def dequantize_mxfp4(q, e, out=None, stream=None):
     dev = step.device(q, "q")
     if out is None:
         import torch
+        if q.ndim < 1:
+            raise ValueError("q must be [.., k/2], got []")
         out = _new(tuple(q.shape[:-1]) + (2 * q.shape[-1],), torch.float32, q, stream)
     _run(step.dequantize_mxfp4, dev, stream, q, e, out)
     return out
@@ -818,7 +828,8 @@ def gemm_mxfp4(wq, we, xq, xe, x_scale=None, out=None, stream=None):
     dev = step.device(wq, "wq")
     if out is None:
         import torch
-        out = _new((xq.shape[0], wq.shape[0]), torch.float32, wq, stream)
+        step.device(xq, "xq")
+        out = _new((_matrix(xq, "xq")[0], _matrix(wq, "wq")[0]), torch.float32, wq, stream)
     _run(step.gemm_mxfp4, dev, stream, wq, we, xq, xe, x_scale, out)
     return out
 
@@ -831,7 +842,7 @@ def add_rmsnorm_mxfp4(x, weight, residual=None, eps: float = 1e-5, q=None, e=Non
     dev = step.device(x, "x")
     if q is None or e is None or s is None:
         import torch
-        n, k = x.shape
+        n, k = _matrix(x, "x")
         q = _new((n, k // 2), torch.uint8, x, stream) if q is None else q
         e = _new((n, k // 32), torch.uint8, x, stream) if e is None else e
         s = _new(n, torch.float32, x, stream) if s is None else s

@@ -1,5 +1,5 @@
 """MXFP4 on the GPU at the edges of what its header allows: attention scales and scores near the ends
-of f32."""
+of f32, operands that are missing."""
 
 from __future__ import annotations
 
@@ -91,3 +91,27 @@ def test_attention_bf16_any_scale(scale, q_mul, k_mul):
         k = c["cache"].k
         k.copy_(_torch().where(_torch().isfinite(k), k.float() * k_mul, k.float()))
         of_step._check(c)
+
+
+# ------------------------------------------------------------------ refusals
+def test_missing_and_flat_operands_are_named():
+    torch, qmm = _torch(), _qmm()
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    f32 = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    q, e = u8(4, 32), u8(4, 2)
+    for call, error, name in (
+        (lambda: qmm.gemm_mxfp4(q, e, None, e), TypeError, "xq"), (lambda: qmm.gemm_mxfp4(q, e, q, None), TypeError, "xe"),
+        (lambda: qmm.gemm_mxfp4(None, e, q, e), TypeError, "wq"), (lambda: qmm.gemm_mxfp4(q, None, q, e), TypeError, "we"),
+        (lambda: qmm.gemm_mxfp4(q, e, u8(4)[0], e), ValueError, "xq"), (lambda: qmm.gemm_mxfp4(u8(4)[0], e, q, e), ValueError, "wq"),
+        (lambda: qmm.gemm_mxfp4(q, e, u8(32), u8(2)), ValueError, "xq"), (lambda: qmm.gemm_mxfp4(q, e, q, e, x_scale=3.0), TypeError, "x_scale"),
+        (lambda: qmm.quantize_mxfp4(None), TypeError, "x"), (lambda: qmm.quantize_mxfp4(f32(64)), ValueError, "x must"),
+        (lambda: qmm.quantize_mxfp4(f32(4)[0]), ValueError, "x must"), (lambda: qmm.quantize_mxfp4(f32(2, 2, 32)), ValueError, "x must"),
+        (lambda: qmm.dequantize_mxfp4(None, e), TypeError, "q"), (lambda: qmm.dequantize_mxfp4(q, None), TypeError, "e"),
+        (lambda: qmm.dequantize_mxfp4(u8(4)[0], e), ValueError, "q must"),
+        (lambda: qmm.add_rmsnorm_mxfp4(None, f32(64)), TypeError, "x"), (lambda: qmm.add_rmsnorm_mxfp4(f32(4, 64), None), TypeError, "weight"),
+        (lambda: qmm.add_rmsnorm_mxfp4(f32(64), f32(64)), ValueError, "x must"),
+        (lambda: qmm.add_rmsnorm_mxfp4(f32(4)[0], f32(64)), ValueError, "x must"),
+        (lambda: qmm.add_rmsnorm_mxfp4(f32(1, 4, 64), f32(64)), ValueError, "x must"),
+    ):
+        with pytest.raises(error, match=name):
+            call()
