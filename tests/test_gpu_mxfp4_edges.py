@@ -1,5 +1,5 @@
-"""MXFP4 on the GPU at the edges of what its header allows: attention scales and scores near the ends
-of f32, operands that are missing."""
+"""MXFP4 on the GPU at the edges of what its header allows: attention scales, scores and queries,
+products and arrays that pass a launch's limits, every kernel's tails, operands that are missing."""
 
 from __future__ import annotations
 
@@ -91,6 +91,123 @@ def test_attention_bf16_any_scale(scale, q_mul, k_mul):
         k = c["cache"].k
         k.copy_(_torch().where(_torch().isfinite(k), k.float() * k_mul, k.float()))
         of_step._check(c)
+
+
+# ------------------------------------------------------------------ product
+def _exact_check(m, k, n, seed=0, nan=True):
+    """A product whose sums are exact (scales 1 and 2: multiples of 1/4, below 2^24 / 4)."""
+    torch, qmm = _torch(), _qmm()
+    rng = np.random.default_rng(seed + m * 7 + k + n)
+    w, x = (rng.integers(0, 256, (r, k // 2), dtype=np.uint8) for r in (m, n))
+    we, xe = (rng.integers(127, 129, (r, k // 32), dtype=np.uint8) for r in (m, n))
+    out = torch.full((n + 1, m + 3), 7.0, device="cuda")
+    qmm.gemm_mxfp4(_dev(w), _dev(we), _dev(x), _dev(xe), out=out[:n, :m])
+    got = out.cpu().numpy()
+    assert np.array_equal(got[:n, :m], mxfp4.gemm(w, we, x, xe)[0]), (m, k, n)
+    assert (got[n] == 7).all() and (got[:, m:] == 7).all()
+    if nan:         # a NaN scale at a row's and a token's end stays in them
+        we[m // 2, -1] = xe[n // 2, -1] = 255
+        got = qmm.gemm_mxfp4(*(_dev(a) for a in (w, we, x, xe))).cpu().numpy()
+        bad = np.zeros((n, m), bool)
+        bad[n // 2] = bad[:, m // 2] = True
+        assert np.array_equal(np.isnan(got), bad), (m, k, n)
+
+
+@pytest.mark.parametrize("kernel", range(11))
+def test_gemm_every_kernel_where_each_can_run(kernel, monkeypatch):
+    """k in whole 64s, which every kernel takes (8 and 9 take no other): whole passes and then part of
+    one, in rows and tokens that end inside a tile."""
+    monkeypatch.setenv("QMM_MX_KERNEL", str(kernel))
+    for m, k, n in [(33, 320, 35), (1, 1088, 1), (47, 2112, 17), (130, 576, 70), (300, 1344, 257), (16, 4160, 33),
+                    (31, 192, 64), (70, 3136, 290), (513, 640, 45)]:
+        gh.note(f"gemm_mxfp4 kernel {kernel} {m}x{k} n={n}")
+        _exact_check(m, k, n)
+
+
+@pytest.mark.parametrize("kernel", [None, 5, 7, 8, 10])
+def test_gemm_more_token_tiles_than_a_grid_axis(kernel, monkeypatch):
+    """2^20 tokens are 65536 tiles of 16, one more than a grid's second axis takes: for one row and this
+    k kernel 10 would be the fastest, and 8 and 10 may not be forced either."""
+    if kernel is not None:
+        monkeypatch.setenv("QMM_MX_KERNEL", str(kernel))
+    torch, qmm = _torch(), _qmm()
+    n, k = 1 << 20, 1024
+    gh.note(f"gemm_mxfp4 kernel {kernel} 1x{k} n={n}")
+    torch.manual_seed(5)
+    w, x = (torch.randint(0, 256, (r, k // 2), dtype=torch.uint8, device="cuda") for r in (1, n))
+    we, xe = (torch.randint(127, 129, (r, k // 32), dtype=torch.uint8, device="cuda") for r in (1, n))
+    got = qmm.gemm_mxfp4(w, we, x, xe)
+    want = torch.cat([(qmm.dequantize_mxfp4(x[i:i + 65536], xe[i:i + 65536]) * qmm.dequantize_mxfp4(w, we)).sum(1)
+                      for i in range(0, n, 65536)])
+    assert torch.equal(got[:, 0], want)
+
+
+@pytest.mark.parametrize("kernel", [None, 5, 7, 8, 10])
+def test_gemm_more_tiles_than_a_grid(kernel, monkeypatch):
+    """66000 x 66000 outputs are 4125^2 tiles of 16 x 16 or half as many of 32 x 16, more than the 2^22
+    work groups that a launch takes (2^32 threads and more of the smallest): those kernels leave it to
+    others."""
+    if kernel is not None:
+        monkeypatch.setenv("QMM_MX_KERNEL", str(kernel))
+    torch, qmm = _torch(), _qmm()
+    m = n = 66000
+    gh.note(f"gemm_mxfp4 kernel {kernel} {m}x64 n={n}")
+    torch.manual_seed(6)
+    w, x = (torch.randint(0, 256, (r, 32), dtype=torch.uint8, device="cuda") for r in (m, n))
+    we, xe = (torch.randint(127, 129, (r, 2), dtype=torch.uint8, device="cuda") for r in (m, n))
+    out = torch.full((n, m), float("nan"), device="cuda")
+    qmm.gemm_mxfp4(w, we, x, xe, out=out)
+    assert not torch.isnan(out).any()
+    wf, xf = qmm.dequantize_mxfp4(w, we), qmm.dequantize_mxfp4(x, xe)
+    at = torch.randint(0, n, (24,)).tolist() + [0, 15, 16, 32767, 32768, 65535, 65536, n - 1]
+    for i in at:
+        assert torch.equal(out[i], (wf * xf[i]).sum(1)), i
+        assert torch.equal(out[:, i], (xf * wf[i]).sum(1)), i
+
+
+@pytest.mark.parametrize("n", [3, 40, 300])
+def test_gemm_codes_of_zero_under_far_scales(n):
+    """0 times anything is 0, whatever the two scales' product: 2^254 where all codes of one side are
+    zero, beside blocks of ordinary size."""
+    torch, qmm = _torch(), _qmm()
+    rng = np.random.default_rng(n)
+    m, k = 70, 1152
+    w, x = (rng.integers(0, 256, (r, k // 2), dtype=np.uint8) for r in (m, n))
+    we, xe = (rng.integers(127, 129, (r, k // 32), dtype=np.uint8) for r in (m, n))
+    for blk in range(0, k // 32, 3):
+        we[:, blk] = xe[:, blk] = 254
+        (w if blk % 2 else x)[:, 16 * blk:16 * blk + 16] &= 0x88        # zeros of either sign
+    want = mxfp4.gemm(w, we, x, xe)[0]
+    assert np.isfinite(want).all() and np.array_equal(qmm.gemm_mxfp4(*(_dev(a) for a in (w, we, x, xe))).cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ quantization
+def test_quantize_more_items_than_a_grid():
+    """2^35 values and some are four times as many items of eight as a launch has threads, and more than
+    32 bits count; 2^33 values back are twice as many items of four."""
+    torch, qmm = _torch(), _qmm()
+    k = 1 << 16
+    rows = (1 << 19) + 3
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("less than 120 GiB of device memory free")
+    gh.note(f"quantize bfloat16 {rows}x{k}")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    some = torch.randn(4099, k, device="cuda", generator=gen).bfloat16()       # rows that repeat at no power of two
+    x = torch.empty(rows, k, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, rows, 4099):
+        x[i:i + 4099] = some[:rows - i]
+    q, e = qmm.quantize_mxfp4(x)
+    del x
+    sq, se = qmm.quantize_mxfp4(some)           # a launch of one step
+    for i in range(0, rows, 4099):
+        assert torch.equal(q[i:i + 4099], sq[:rows - i]) and torch.equal(e[i:i + 4099], se[:rows - i]), i
+    wq, we = mxfp4.quantize(some[:2, :4096].float().cpu().numpy())
+    assert np.array_equal(sq[:2, :2048].cpu().numpy(), wq) and np.array_equal(se[:2, :128].cpu().numpy(), we)
+    rows = (1 << 17) + 3
+    gh.note(f"dequantize {rows}x{k}")
+    back, want = qmm.dequantize_mxfp4(q[:rows], e[:rows]), qmm.dequantize_mxfp4(sq, se)
+    for i in range(0, rows, 4099):
+        assert torch.equal(back[i:i + 4099], want[:rows - i]), i
 
 
 # ------------------------------------------------------------------ refusals
