@@ -7,8 +7,8 @@ import numpy as np
 import pytest
 
 import gpu_helpers as gh
-from oracle import mxfp4
-from test_gpu_mxfp4 import _case, _check, _dev, _qmm, _torch
+from oracle import mxfp4, step
+from test_gpu_mxfp4 import _case, _check, _dev, _qmm, _torch, _want
 
 pytestmark = pytest.mark.gpu
 
@@ -91,6 +91,41 @@ def test_attention_bf16_any_scale(scale, q_mul, k_mul):
         k = c["cache"].k
         k.copy_(_torch().where(_torch().isfinite(k), k.float() * k_mul, k.float()))
         of_step._check(c)
+
+
+@pytest.mark.parametrize("far", [2.0 ** 6, 2.0 ** 10, 2.0 ** 14, 2.0 ** 20])
+@pytest.mark.parametrize("d", [32, 96, 128, 256])
+def test_attention_one_large_query_element(d, far):
+    """One element of a block many times the others, where most keys hold a zero: an element is kept
+    to 2^-29 of its block's largest, so a token's score is off by E = |scale| 2^-29 sum over blocks of
+    max|q| sum|k| beside what the oracle allows, a weight by the factor exp(E), an output by
+    (exp(2 E) - 1) max|v|, the log-sum-exp by E."""
+    gh.note(f"attention mxfp4 d={d} an element *{far}")
+    torch, qmm = _torch(), _qmm()
+    for page in (16, 2):
+        c = _case([70, 0, 33, 100], 2, 3, d, page, scales=(118, 123))
+        at = (7 + 32 * np.arange(d // 32)) % d
+        c["q"][:, :, at] *= np.float32(far)
+        codes = c["host"]["k"]
+        codes[..., at // 2] &= np.where(at % 2, 0x0f, 0xf0).astype(np.uint8)       # their keys' codes
+        first = c["table"][0][0]
+        codes[first, :, 1, at[0] // 2] |= np.uint8(2 << 4 * (at[0] % 2))           # but one
+        c["cache"].k.copy_(_dev(codes))
+        lse = torch.empty(4, 6, device="cuda")
+        out = qmm.paged_attention(_dev(c["q"]), c["cache"], _dev(c["table"]),
+                                  torch.tensor(c["lens"], dtype=torch.int32, device="cuda"), scale=c["scale"], lse=lse)
+        for i, n in enumerate(c["lens"]):
+            if n == 0:
+                continue
+            want, wl, tol, top, vtop = _want(c, i)
+            t = np.arange(n)
+            where = (c["table"][i][t // c["page"]], slice(None), t % c["page"])
+            k = np.abs(mxfp4.dequantize(c["host"]["k"][where], c["host"]["ks"][where])).reshape(n, 2, d // 32, 32).sum(-1)
+            m = np.abs(c["q"][i].astype(np.float64)).reshape(6, d // 32, 32).max(-1)
+            e = 2.0 ** -29 * c["scale"] * (k[:, np.arange(6) // 3] * m).sum(-1).max(0)       # of each head
+            assert np.all(np.abs(out[i].cpu().numpy() - want) <= tol + (np.expm1(2 * e) * vtop)[:, None]), i
+            reach = c["scale"] * np.abs(c["q"][i]).sum(-1) * top
+            assert np.all(np.abs(lse[i].cpu().numpy() - wl) <= step.lse_tol(wl, n, reach, d) + e), i
 
 
 # ------------------------------------------------------------------ product
