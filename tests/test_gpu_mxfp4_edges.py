@@ -8,7 +8,7 @@ import pytest
 
 import gpu_helpers as gh
 from oracle import mxfp4, step
-from test_gpu_mxfp4 import _case, _check, _dev, _qmm, _torch, _want
+from test_gpu_mxfp4 import _case, _check, _dev, _flushed, _layer, _layer_state, _qmm, _torch, _want
 
 pytestmark = pytest.mark.gpu
 
@@ -216,6 +216,59 @@ def test_gemm_codes_of_zero_under_far_scales(n):
     assert np.isfinite(want).all() and np.array_equal(qmm.gemm_mxfp4(*(_dev(a) for a in (w, we, x, xe))).cpu().numpy(), want)
 
 
+# ------------------------------------------------------------------ cache
+@pytest.mark.parametrize("page,n_pages,strides,scale_strides,at", [
+    # pages a GiB apart, up to the 64 GiB that a cache may span: codes of both, then scales of both, in each
+    (16, 63, (1 << 30, 1 << 12, 64), (1 << 30, 1 << 12, 16), (0, 1 << 28, 1 << 29, 3 << 28)),
+    (4, 63, (1 << 30, 1 << 12, 64), (1 << 30, 1 << 12, 16), (0, 1 << 28, 1 << 29, 3 << 28)),
+    # a page's tokens 128 MiB apart and a little less, beside and within what 32-bit offsets of 16 rows take
+    (16, 4, (1 << 16, 1 << 12, 1 << 27), (1 << 16, 1 << 12, 1 << 27), (0, 1 << 20, 1 << 21, 3 << 20)),
+    (16, 4, (1 << 16, 1 << 12, (1 << 27) - 64), (1 << 16, 1 << 12, (1 << 27) - 63), (0, 1 << 20, 1 << 21, 3 << 20)),
+    (32, 4, (1 << 16, 1 << 12, (1 << 27) - 64), (1 << 16, 1 << 12, (1 << 27) - 63), (0, 1 << 20, 1 << 21, 3 << 20)),
+])
+def test_rows_far_apart(page, n_pages, strides, scale_strides, at):
+    """Append and attention where rows and scales are as far apart as a cache may hold them."""
+    torch, qmm = _torch(), _qmm()
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("less than 80 GiB of device memory free")
+    gh.note(f"mxfp4 cache page {page} x {n_pages} strides {strides}")
+    n_kv, group, d = 2, 3, 96
+    sizes = (n_pages, n_kv, page)
+    reach = max(sum((n - 1) * s for n, s in zip(sizes, st)) for st in (strides, scale_strides)) + max(at) + d
+    base = torch.empty(reach, dtype=torch.uint8, device="cuda")
+    k, v, ks, vs = (base.as_strided(sizes + (w,), st + (1,), o) for w, st, o in
+                    zip((d // 2, d // 2, d // 32, d // 32), (strides, strides, scale_strides, scale_strides), at))
+    cache = qmm.KVCache(k, v, ks, vs)
+    rng = np.random.default_rng(page + n_pages)
+    lens = [n_pages * page // 2 - 5, 7, n_pages * page // 4]
+    pages = [-(-n // page) for n in lens]
+    ids = rng.permutation(n_pages)
+    ids = np.concatenate([[n_pages - 1, 0], ids[(ids != 0) & (ids != n_pages - 1)]])
+    table, slots, used = np.full((3, max(pages)), -1, np.int32), [], 0
+    for i, (n, p) in enumerate(zip(lens, pages)):
+        table[i, :p] = ids[used:used + p]
+        used += p
+        t = np.arange(n)
+        slots.append(table[i][t // page] * page + t % page)
+    slots = np.concatenate(slots).astype(np.int32)
+    kv = rng.normal(size=(2, len(slots), n_kv, d)).astype(np.float32)
+    qmm.kv_append(cache, _dev(kv[0]), _dev(kv[1]), _dev(slots))
+    p, s = _dev(slots // page).long(), _dev(slots % page).long()
+    held = []
+    for rows, codes, scales in ((kv[0], k, ks), (kv[1], v, vs)):
+        wq, we = mxfp4.quantize(rows.reshape(-1, d))
+        assert np.array_equal(codes[p, :, s].cpu().numpy().reshape(-1, d // 2), wq)
+        assert np.array_equal(scales[p, :, s].cpu().numpy().reshape(-1, d // 32), we)
+        held.append(mxfp4.dequantize(wq, we).reshape(rows.shape))
+    q = rng.normal(size=(3, n_kv * group, d)).astype(np.float32)
+    out = qmm.paged_attention(_dev(q), cache, _dev(table), torch.tensor(lens, dtype=torch.int32, device="cuda")).cpu().numpy()
+    first = 0
+    for i, n in enumerate(lens):
+        want, _, tol = step.attention(q[i], held[0][first:first + n], held[1][first:first + n], d ** -0.5)
+        assert np.all(np.abs(out[i] - want) <= tol + _flushed(n, np.abs(held[1]).max())), i
+        first += n
+
+
 # ------------------------------------------------------------------ quantization
 def test_quantize_more_items_than_a_grid():
     """2^35 values and some are four times as many items of eight as a launch has threads, and more than
@@ -243,6 +296,35 @@ def test_quantize_more_items_than_a_grid():
     back, want = qmm.dequantize_mxfp4(q[:rows], e[:rows]), qmm.dequantize_mxfp4(sq, se)
     for i in range(0, rows, 4099):
         assert torch.equal(back[i:i + 4099], want[:rows - i]), i
+
+
+# ------------------------------------------------------------------ together
+def test_layers_at_the_same_time_and_in_two_graphs():
+    """Three layers with inputs of their own on three streams at once, and two graphs replayed in turn:
+    each as it is alone."""
+    torch = _torch()
+    states = [_layer_state(seed=s)[0] for s in (11, 12, 13)]
+    alone = [[t.clone() for t in _layer(st)] for st in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(5):
+        got = [_layer(st, stream=s) for st, s in zip(states, streams)]
+        torch.cuda.synchronize()
+        for mine, want in zip(got, alone):
+            assert all(torch.equal(a, b) for a, b in zip(mine, want))
+    graphs = []
+    for st, s in zip(states[:2], streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            held = _layer(st)
+        graphs.append((graph, held))
+    for _ in range(3):
+        for graph, _held in graphs:
+            graph.replay()
+        again = _layer(states[2])
+        torch.cuda.synchronize()
+        for mine, want in zip([held for _, held in graphs] + [again], alone):
+            assert all(torch.equal(a, b) for a, b in zip(mine, want))
 
 
 # ------------------------------------------------------------------ refusals
