@@ -69,6 +69,9 @@ constexpr int HEADS = 16;     // query heads per pass over a unit's rows
 // (8-bit: 64 KB) of loads in flight on a CU, and more read no faster: with
 // three or four, where the registers allow it, 8-bit heads of 128 went from
 // 103 to 121 us and f16 heads of 64 from 92 to 97 us (64 sequences of 4096).
+// MXFP4 rows take two at every size: heads of 192, 224 and 256 keep up to 34
+// registers in scratch for it and are the faster (59, 70 and 69 us for 69, 78 and
+// 79 with one and none in scratch, 32 sequences of 4096 with 8 kv heads).
 constexpr int occupancy(int kind, int nb) { return kind == KV_MX4 || nb <= (kind == KV_Q8 ? 6 : 5) ? 2 : 1; }
 // What a unit's start and end cost its wave, in tiles: its loads are not ahead
 // of it, and its sums are written.  Counted where a wave has at least
@@ -672,7 +675,7 @@ __device__ __forceinline__ f32x4 mfma_parts(u32x4 k, uint32_t ks, u32x6 q, uint3
 // 44 for p's parts) and 36 of the matrix cores, which keep the two busy for 45 and 22 of
 // 100 cycles, one after the other in a wave, with two waves a SIMD.  Rows of 64 bytes
 // with tokens outermost ask L2 for each line twice and read 12% more from HBM: the
-// ragged sequences take 106 us so, 90 with heads outermost.  Three tiles in flight, a
+// ragged sequences take 103 us so, 88 with heads outermost.  Three tiles in flight, a
 // third work group a CU, and other orders of the heads over the XCDs gave nothing or lost.
 //
 // Loads in flight.  A tile's arithmetic is shorter than a load's way, so what matters

@@ -7,10 +7,11 @@
 // bytes) of operand row i, any block, as long as both operands' lanes c hold the
 // same one; and rows 4c .. 4c + 3 of output column i.
 //
-// Bounds and measured times (MI355X, operands in HBM).  Few tokens: the weights'
-// bytes, 14336 x 4096 with 16 tokens (32 MB) 7.6 us, 4.2 TB/s; or latency, 4608 x
-// 1024 with one 3.2 us, 1024 x 4608 with 512 6.8 us.  Many, 14336 x 4096 with 2048:
-// 76.0 us, 3.16 PFLOP/s, where the matrix instructions alone take 44 to 51 us (the
+// Bounds and measured times (MI355X).  Few tokens: the weights' bytes, 14336 x
+// 4096 with 16 tokens (32 MB) 8.9 us from HBM, 3.6 TB/s, 7.6 where the 256 MB cache
+// holds them; or latency, 4608 x 1024 with one 3.2 us, 1024 x 4608 with 512 6.8
+// us.  In between, 4096 x 4096 with 512, 13.9: 128 tiles of 128 x 128 for 256 CUs, or
+// 64 x 64 ones, which read twice the bytes.  Many, 14336 x 4096 with 2048: 76.0 us, 3.16 PFLOP/s, where the matrix instructions alone take 44 to 51 us (the
 // clock falls with the data), the loads into LDS alone 54 us (L2 gives about 15 TB/s
 // of whole lines) and the outputs, behind which no loads go on, 13 to 19 us; operands'
 // reads from LDS and the loads' writes keep it as busy as the matrix cores are.
@@ -136,7 +137,7 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 
 // A work group of WM x WN waves takes BM = 16 RI WM weight rows x BN = 16 NJ WN
 // tokens.  Codes go in stages of 256 k, a 128-byte line of each row, from memory
-// straight into two stages of LDS; chunk p of row r holds chunk p ^ (r / 2 % 8), so
+// straight into NR stages of LDS; chunk p of row r holds chunk p ^ (r / 2 % 8), so
 // that the 16 rows a wave reads at a time lie in different banks.  Scales, 16
 // bytes a row for 512 k, go through registers, where they are turned so that a
 // lane's four steps are the bytes of one word.
@@ -433,9 +434,11 @@ void stream(const MxGemmArgs& a, hipStream_t st) {
 // work groups one after another on a CU that holds `per_cu` at a time, and a
 // load of work groups per CU (at least 1; whole where one fits a CU).  The four
 // are fitted to the times of 522 products, m 16 .. 14336, k 64 .. 14336, n 1 ..
-// 4096, in graphs with the operands in HBM (7 to 17% rms error a kernel where it
-// is within 1.7 of the fastest); the kernel with the least takes 2.7% longer than
-// the fastest of all on average, 49% at worst.
+// 4096, in graphs with the operands in HBM.  On 520 products timed since, most of
+// them in the 256 MB cache, they are 11 to 26% off (rms; the last three, from
+// memory, up to 37%) where a kernel is within 1.7 of the fastest; the kernel with
+// the least takes 0.7% longer than the fastest of all on 90 projections, 22% at
+// worst, and 2.4% on 430 sizes spread over their logarithms, 51% at worst.
 struct Kernel {
     void (*launch)(const MxGemmArgs&, hipStream_t);
     int rows, tokens, k_groups, per_cu, pass;
