@@ -914,14 +914,16 @@ struct SegmentMx {
             const float alpha = __builtin_amdgcn_exp2f(m - base);
             m = top;
             float p[8], sum = 0.0f;
-            if (__any(fabsf(base) >= 0x1p20f)) {
+            const bool far = fabsf(base) >= 0x1p20f;
+            if (__any(far)) {
                 // a maximum rounded by 1/16 and more: scores rounded alike are at most as large, where
                 // the exact products below may be ahead of it by more than an exponential holds
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float x = s[j] * qs;
                     asm("" : "+v"(x));  // rounded
-                    p[j] = __builtin_amdgcn_exp2f(x - base + pbits);
+                    // (the other heads of the wave as below: their bits do not depend on this one)
+                    p[j] = __builtin_amdgcn_exp2f(far ? x - base + pbits : __builtin_fmaf(s[j], qs, shift));
                 }
             } else {
 #pragma unroll

@@ -52,6 +52,21 @@ def test_attention_any_score(q_mul, page):
     assert seen > 50
 
 
+def test_attention_heads_do_not_touch_each_other():
+    """A head whose scores are far larger leaves the others' bits as they are."""
+    torch, qmm = _torch(), _qmm()
+    for page, tokens in ((16, 0), (4, 1024)):
+        c = _case([700 if tokens else 70, 33], 2, 4, 64, page, tokens=tokens, scale=0.125)
+        args = (c["cache"], _dev(c["table"]), torch.tensor(c["lens"], dtype=torch.int32, device="cuda"))
+        alone = qmm.paged_attention(_dev(c["q"]), *args, scale=0.125)
+        for head in (0, 3, 6):
+            q = c["q"].copy()
+            q[:, head] *= np.float32(2.0 ** 40)
+            out = qmm.paged_attention(_dev(q), *args, scale=0.125)
+            keep = [h for h in range(8) if h != head]
+            assert torch.isfinite(out).all() and torch.equal(out[:, keep], alone[:, keep])
+
+
 @pytest.mark.parametrize("page", [16, 4])
 @pytest.mark.parametrize("scale,q_mul,scales", [
     (2.0 ** -30, 2.0 ** 20, (238, 243)),      # sums of products beyond f32, scores of 2^110
