@@ -11,10 +11,11 @@
 // 4096 with 16 tokens (32 MB) 8.9 us from HBM, 3.6 TB/s, 7.6 where the 256 MB cache
 // holds them; or latency, 4608 x 1024 with one 3.2 us, 1024 x 4608 with 512 6.8
 // us.  In between, 4096 x 4096 with 512, 13.9: 128 tiles of 128 x 128 for 256 CUs, or
-// 64 x 64 ones, which read twice the bytes.  Many, 14336 x 4096 with 2048: 76.0 us, 3.16 PFLOP/s, where the matrix instructions alone take 44 to 51 us (the
-// clock falls with the data), the loads into LDS alone 54 us (L2 gives about 15 TB/s
-// of whole lines) and the outputs, behind which no loads go on, 13 to 19 us; operands'
-// reads from LDS and the loads' writes keep it as busy as the matrix cores are.
+// 64 x 64 ones, which read twice the bytes.  Many, 14336 x 4096 with 2048: 76.0 us,
+// 3.16 PFLOP/s, where the matrix instructions alone take 44 to 51 us (the clock falls
+// with the data), the loads into LDS alone 54 us (L2 gives about 15 TB/s of whole
+// lines) and the outputs, behind which no loads go on, 13 to 19 us; operands' reads
+// from LDS and the loads' writes keep it as busy as the matrix cores are.
 // In turn: operands straight from memory 656 us; 128 x 128 tiles through LDS 126;
 // scales as 16 bytes a row 98; whole lines of outputs past the caches 90; lines of
 // 128 bytes with operands read ahead 85; outputs through LDS and 256 x 256 tiles 79.5;

@@ -80,6 +80,7 @@ def test_attention_heads_do_not_touch_each_other():
     (0.0, 2.0 ** 100, (120, 129)),
     (2.0 ** -126, 2.0 ** 120, (246, 252)),    # products of 2^244
     (3e38, 2.0 ** 60, (0, 3)),
+    (2.0 ** 126, 2.0 ** 118, (0, 1)),
 ])
 def test_attention_any_scale(scale, q_mul, scales, page):
     """Finite elements and scores give finite outputs whatever the scale."""
@@ -96,7 +97,8 @@ def test_attention_any_scale(scale, q_mul, scales, page):
 @pytest.mark.parametrize("scale,q_mul,k_mul", [
     (2.0 ** -30, 2.0 ** 20, 2.0 ** 115), (-2.0 ** -100, 2.0 ** 60, 2.0 ** 120), (2.0 ** 118, 1.0, 2.0 ** -118),
     (-3e38, 2.0 ** -3, 2.0 ** -120), (3e38, 1e-37, 0.1), (2.0 ** 60, 2.0 ** 50, 2.0 ** -110),
-    (2.0 ** -149, 2.0 ** 120, 2.0 ** 26), (0.0, 2.0 ** 60, 1.0), (0.125, 2.0 ** 33, 1.0), (-0.125, 2.0 ** 100, 1.0)])
+    (2.0 ** -149, 2.0 ** 120, 2.0 ** 26), (2.0 ** 126, 2.0 ** 118, 2.0 ** -125),
+    (0.0, 2.0 ** 60, 1.0), (0.125, 2.0 ** 33, 1.0), (-0.125, 2.0 ** 100, 1.0)])
 def test_attention_bf16_any_scale(scale, q_mul, k_mul):
     """The same of a bfloat16 cache."""
     import test_gpu_step as of_step
@@ -106,6 +108,15 @@ def test_attention_bf16_any_scale(scale, q_mul, k_mul):
         k = c["cache"].k
         k.copy_(_torch().where(_torch().isfinite(k), k.float() * k_mul, k.float()))
         of_step._check(c)
+
+
+@pytest.mark.parametrize("kind,scale,q_mul,kv_mul", [("f16", 2.0 ** 118, 2.0 ** 16, 2.0 ** -16), ("f16", -2.0 ** 30, 2.0 ** 100, 2.0 ** -14),
+                                                     ("q8", 2.0 ** 118, 2.0 ** 16, 2.0 ** -16), ("q8", 2.0 ** 20, 2.0 ** 110, 2.0 ** -12)])
+def test_attention_f16_and_8_bit_largest_products_of_scale_and_query(kind, scale, q_mul, kv_mul):
+    import test_gpu_step as of_step
+    gh.note(f"attention {kind} scale {scale} q*{q_mul}")
+    for lens, tokens in (([70, 1, 0, 33], 0), ([700, 90], 1024)):
+        of_step._check(of_step._case(kind, lens, 2, 4, 64, 16, tokens=tokens, scale=scale, q_mul=q_mul, kv_mul=kv_mul))
 
 
 @pytest.mark.parametrize("far", [2.0 ** 6, 2.0 ** 10, 2.0 ** 14, 2.0 ** 20])
